@@ -8,6 +8,8 @@ library's CUDA kernels. PyTorch supplies device memory and streams.
     prefill(...)        whole forward for B sequences of L tokens
     decode(...)         one new token per sequence over the latent cache
     latent_expand(...)  latent RMSNorm + W_UKV expansion + rotary-key RoPE
+    qcache_write / qcache_read / qcache_expand / qcache_decode(...)
+                        the latent cache in 8 bits: written, read back, expanded, decoded over
     rope_tables(...)    the cos/sin tables the kernels read (set-up, like weights)
 """
 from __future__ import annotations
@@ -22,7 +24,8 @@ from ._abi import GDLA_BF16, GDLA_FP32, GDLA_MASK_CAUSAL, GDLA_MASK_SLIDING, Gdl
 
 __all__ = ["prefill", "prefill_host", "prefill_host_workspace_size", "gates", "attend", "decode", "decode_noalloc", "latent_expand", "rope_tables", "yarn_rope_tables",
            "yarn_mscale", "prefill_workspace_size", "decode_workspace_size", "workspace_status", "diag_wait_timeout",
-           "build_info", "GdlaError"]
+           "build_info", "GdlaError", "qcache_empty", "qcache_scale_blocks", "qcache_write", "qcache_read", "qcache_expand",
+           "qcache_decode", "qcache_decode_workspace_size"]
 
 _DT = {torch.bfloat16: GDLA_BF16, torch.float32: GDLA_FP32}
 
@@ -334,6 +337,183 @@ def decode_noalloc(c_cache, kr_cache, q, w_ukv, rope_cos, rope_sin, lam_logits, 
     a = _decode_args(c_cache, kr_cache, q, w_ukv, rope_cos, rope_sin, lam_logits, gate_logits, seqlens, out, g,
                      mask, window, softmax_scale, None)
     _abi.check(_lib().gdla_decode_noalloc(ctypes.byref(a), _stream(stream)), "gdla_decode_noalloc")
+    return out
+
+
+# ----------------------------------------------------------- 8-bit latent cache
+_Q8 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def qcache_scale_blocks(T_max: int, scale_block: int) -> int:
+    """Scales of one sequence of a T_max-token 8-bit cache: ceil(T_max / scale_block)."""
+    n = int(_lib().gdla_qcache_scale_blocks(int(T_max), int(scale_block)))
+    if n < 1:
+        raise ValueError("T_max must be at least 1 and scale_block a power of two in 1 .. 128")
+    return n
+
+
+def qcache_empty(B: int, T_max: int, *, d_c: int = 512, d_rope: int = 64, scale_block: int = 1, device="cuda"):
+    """Memory for an 8-bit cache, not initialised: (c_cache [B,T_max,d_c] and
+    kr_cache [B,T_max,d_rope] in float8_e4m3fn, scales [B,ceil(T_max/scale_block)] fp32)."""
+    return (torch.empty((B, T_max, d_c), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((B, T_max, d_rope), dtype=torch.float8_e4m3fn, device=device),
+            torch.empty((B, qcache_scale_blocks(T_max, scale_block)), dtype=torch.float32, device=device))
+
+
+def _qcache_dims(c_cache, kr_cache, scales, scale_block):
+    if c_cache.dtype not in _Q8 or kr_cache.dtype not in _Q8:
+        raise ValueError("an 8-bit cache is float8_e4m3fn (or its bytes as uint8)")
+    B, T_max, d_c = c_cache.shape
+    if tuple(kr_cache.shape[:2]) != (B, T_max):
+        raise ValueError("c_cache and kr_cache must be [B, T_max, ...] of the same B and T_max")
+    if scales.dtype != torch.float32 or tuple(scales.shape) != (B, qcache_scale_blocks(T_max, scale_block)):
+        raise ValueError("scales must be fp32 [B, ceil(T_max / scale_block)]")
+    return B, T_max, d_c, kr_cache.shape[2]
+
+
+def _same(t, name, shape, dtype=None):
+    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
+        raise ValueError(f"{name} must be {list(shape)}" + (f" {dtype}" if dtype is not None else ""))
+
+
+def _call(fn, a, tensors, stream, what):
+    """The call with the tensors' device current, on ``stream`` or that device's current stream."""
+    t = tensors[0]
+    if any(x is not None and x.device != t.device for x in tensors):
+        raise ValueError("the tensors of a call must be on one device")
+    if stream is None:
+        stream = torch.cuda.current_stream(t.device)
+    if t.device.index == torch.cuda.current_device():
+        _abi.check(fn(ctypes.byref(a), _stream(stream)), what)
+    else:
+        with torch.cuda.device(t.device):
+            _abi.check(fn(ctypes.byref(a), _stream(stream)), what)
+
+
+def qcache_write(c_cache, kr_cache, scales, c_kv, k_rope, *, gamma=None, rope_cos=None, rope_sin=None, start=None,
+                 lens=None, scale_block: int = 1, rms_eps: float = 0.0, workspace=None, stream=None) -> None:
+    """Write new tokens into the 8-bit cache (in place): latent RMSNorm, RoPE of
+    the rotary key at its position, quantisation to e4m3 with a scale per
+    ``scale_block`` tokens.
+
+    c_kv [B,L,d_c] and k_rope [B,L,d_rope] hold up to L new tokens per sequence;
+    sequence b's first lens[b] (all L without ``lens``) go to positions start[b],
+    start[b]+1, ... (0 without ``start``). ``start`` and ``lens`` are int32 [B] on
+    the device. Without ``gamma`` the rows are taken as normalised and rotated
+    already (prefill's cache_c_hat and cache_k_rope). ``workspace`` is a uint8
+    CUDA tensor of 256 bytes or more; workspace_status(workspace) reports a
+    sequence whose range does not fit its cache (left unwritten)."""
+    B, T_max, d_c, d_rope = _qcache_dims(c_cache, kr_cache, scales, scale_block)
+    L = c_kv.shape[1]
+    _same(c_kv, "c_kv", (B, L, d_c))
+    _same(k_rope, "k_rope", (B, L, d_rope), c_kv.dtype)
+    _same(start, "start", (B,), torch.int32)
+    _same(lens, "lens", (B,), torch.int32)
+    max_pos = 0
+    if gamma is not None:
+        if rope_cos is None or rope_sin is None:
+            raise ValueError("rows to normalise (gamma) also take their rotation: rope_cos and rope_sin")
+        _same(gamma, "gamma", (d_c,), c_kv.dtype)
+        max_pos = rope_cos.shape[0]
+        _same(rope_cos, "rope_cos", (max_pos, d_rope // 2), torch.float32)
+        _same(rope_sin, "rope_sin", (max_pos, d_rope // 2), torch.float32)
+    if workspace is None:
+        workspace = torch.empty(256, dtype=torch.uint8, device=c_kv.device)
+    a = _abi.QcacheWriteArgs(B, L, T_max, d_c, d_rope, int(scale_block), _dtype(c_kv), float(rms_eps), max_pos,
+                             _ptr(c_kv), _ptr(gamma), _ptr(k_rope), _ptr(rope_cos), _ptr(rope_sin), _ptr(start),
+                             _ptr(lens), _ptr(c_cache), _ptr(kr_cache), _ptr(scales), _ptr(workspace),
+                             workspace.numel() * workspace.element_size())
+    _call(_lib().gdla_qcache_write, a, (c_cache, kr_cache, scales, c_kv, k_rope, gamma, rope_cos, rope_sin, start, lens,
+                                        workspace), stream, "gdla_qcache_write")
+
+
+def _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out, n_kv=0,
+                 d_nope=0, d_v=0, w_ukv=None, kv_out=None):
+    B, T_max, d_c, d_rope = _qcache_dims(c_cache, kr_cache, scales, scale_block)
+    if dtype not in _DT:
+        raise ValueError(f"unsupported dtype {dtype}; GDLA takes bfloat16 or float32")
+    _same(lens, "lens", (B,), torch.int32)
+    dev = c_cache.device
+    if c_hat_out is None:
+        c_hat_out = torch.empty((B, length, d_c), dtype=dtype, device=dev)
+    if k_rope_out is None:
+        k_rope_out = torch.empty((B, length, d_rope), dtype=dtype, device=dev)
+    _same(c_hat_out, "c_hat_out", (B, length, d_c), dtype)
+    _same(k_rope_out, "k_rope_out", (B, length, d_rope), dtype)
+    a = _abi.QcacheReadArgs(B, int(length), T_max, int(first), d_c, d_rope, int(scale_block), n_kv, d_nope, d_v,
+                            _DT[dtype], _ptr(c_cache), _ptr(kr_cache), _ptr(scales), _ptr(lens), _ptr(w_ukv),
+                            _ptr(c_hat_out), _ptr(k_rope_out), _ptr(kv_out))
+    return a, c_hat_out, k_rope_out
+
+
+def qcache_read(c_cache, kr_cache, scales, *, length: int, first: int = 0, lens=None, scale_block: int = 1,
+                dtype=torch.bfloat16, c_hat_out=None, k_rope_out=None, stream=None):
+    """Rows first .. first+length-1 of every sequence of an 8-bit cache as
+    ``dtype`` values: (c_hat [B,length,d_c], k_rope [B,length,d_rope]). With
+    ``lens`` (int32 [B] on the device) only the first lens[b] of them are read;
+    the others are zeros."""
+    a, c, k = _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out)
+    _call(_lib().gdla_qcache_read, a, (c_cache, kr_cache, scales, lens, c, k), stream, "gdla_qcache_read")
+    return c, k
+
+
+def qcache_expand(c_cache, kr_cache, scales, w_ukv, *, n_kv: int, d_nope: int, d_v: int, length: int, first: int = 0,
+                  lens=None, scale_block: int = 1, kv_out=None, k_rope_out=None, c_hat_out=None, stream=None):
+    """qcache_read() and the W_UKV expansion of the rows, in the types and
+    layouts of latent_expand(): (kv [B,length,n_kv,d_nope+d_v], k_rope
+    [B,length,d_rope], c_hat [B,length,d_c]). The key side of attend() over a
+    cached prefix."""
+    dtype = w_ukv.dtype
+    _same(w_ukv, "w_ukv", (c_cache.shape[-1], n_kv * (d_nope + d_v)))
+    if kv_out is None:
+        kv_out = torch.empty((c_cache.shape[0], length, n_kv, d_nope + d_v), dtype=dtype, device=c_cache.device)
+    _same(kv_out, "kv_out", (c_cache.shape[0], length, n_kv, d_nope + d_v), dtype)
+    a, c, k = _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out,
+                           n_kv, d_nope, d_v, w_ukv, kv_out)
+    _call(_lib().gdla_qcache_expand, a, (c_cache, kr_cache, scales, lens, w_ukv, c, k, kv_out), stream, "gdla_qcache_expand")
+    return kv_out, k, c
+
+
+def qcache_decode_workspace_size(*, B, T_max, d_c, d_rope, n_kv, d_nope, d_v, g, dtype=torch.bfloat16) -> int:
+    a = _abi.QcacheDecodeArgs()
+    a.B, a.T_max, a.d_c, a.d_rope, a.n_kv, a.d_nope, a.d_v, a.n_noise, a.g = B, T_max, d_c, d_rope, n_kv, d_nope, d_v, n_kv, g
+    a.dtype = _DT[dtype]
+    return int(_lib().gdla_qcache_decode_workspace_size(ctypes.byref(a)))
+
+
+def qcache_decode(c_cache, kr_cache, scales, q, w_ukv, rope_cos, rope_sin, lam_logits, gate_logits, seqlens, *, g: int,
+                  scale_block: int = 1, mask: str = "causal", window: int = 0, softmax_scale: float = 0.0, out=None,
+                  workspace=None, stream=None):
+    """decode() over an 8-bit cache (see qcache_write); returns Y [B, n_signal, d_v].
+    A sequence of length 0 (an empty slot of a padded batch) returns zeros."""
+    B, T_max, d_c, d_rope = _qcache_dims(c_cache, kr_cache, scales, scale_block)
+    H_q, d_qk = q.shape[1], q.shape[2]
+    if H_q % (g + 1):
+        raise ValueError("q must hold g*n_noise signal heads followed by n_noise noise heads")
+    n_kv = H_q // (g + 1)
+    d_nope = d_qk - d_rope
+    d_v = w_ukv.shape[1] // n_kv - d_nope
+    _same(q, "q", (B, H_q, d_qk))
+    _same(w_ukv, "w_ukv", (d_c, n_kv * (d_nope + d_v)), q.dtype)
+    _same(lam_logits, "lam_logits", (B, g * n_kv), torch.float32)
+    _same(gate_logits, "gate_logits", (B, g * n_kv, d_v), q.dtype)
+    _same(seqlens, "seqlens", (B,), torch.int32)
+    _same(rope_cos, "rope_cos", (rope_cos.shape[0], d_rope // 2), torch.float32)
+    _same(rope_sin, "rope_sin", (rope_cos.shape[0], d_rope // 2), torch.float32)
+    if out is None:
+        out = torch.empty((B, g * n_kv, d_v), dtype=q.dtype, device=q.device)
+    _same(out, "out", (B, g * n_kv, d_v), q.dtype)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    a = _abi.QcacheDecodeArgs(B, T_max, d_c, d_rope, n_kv, d_nope, d_v, n_kv, g, int(scale_block), _mask(mask),
+                              int(window), float(softmax_scale), _dtype(q), rope_cos.shape[0], _ptr(seqlens),
+                              _ptr(c_cache), _ptr(kr_cache), _ptr(scales), _ptr(q), _ptr(w_ukv), _ptr(rope_cos),
+                              _ptr(rope_sin), _ptr(lam_logits), _ptr(gate_logits), _ptr(out), _ptr(workspace), ws_bytes)
+    if workspace is None:
+        need = int(_lib().gdla_qcache_decode_workspace_size(ctypes.byref(a)))
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), need
+    _call(_lib().gdla_qcache_decode, a, (c_cache, kr_cache, scales, q, w_ukv, rope_cos, rope_sin, lam_logits, gate_logits,
+                                         seqlens, out, workspace), stream, "gdla_qcache_decode")
     return out
 
 

@@ -56,6 +56,30 @@ class DecodeArgs(ctypes.Structure):
         ("workspace_bytes", ctypes.c_size_t)]
 
 
+class QcacheWriteArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "L", "T_max", "d_c", "d_rope", "scale_block", "dtype")] + [
+        ("rms_eps", ctypes.c_float), ("rope_max_pos", ctypes.c_int),
+        ("c_kv", _vp), ("gamma", _vp), ("k_rope", _vp), ("rope_cos", _vp), ("rope_sin", _vp), ("start", _vp),
+        ("lens", _vp), ("c_cache", _vp), ("kr_cache", _vp), ("scales", _vp), ("workspace", _vp),
+        ("workspace_bytes", ctypes.c_size_t)]
+
+
+class QcacheReadArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "L", "T_max", "first", "d_c", "d_rope", "scale_block", "n_kv",
+                                            "d_nope", "d_v", "dtype")] + [
+        ("c_cache", _vp), ("kr_cache", _vp), ("scales", _vp), ("lens", _vp), ("w_ukv", _vp), ("c_hat_out", _vp),
+        ("k_rope_out", _vp), ("kv_out", _vp)]
+
+
+class QcacheDecodeArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T_max", "d_c", "d_rope", "n_kv", "d_nope", "d_v", "n_noise", "g",
+                                            "scale_block", "mask", "window")] + [
+        ("softmax_scale", ctypes.c_float), ("dtype", ctypes.c_int), ("rope_max_pos", ctypes.c_int),
+        ("seqlens", _vp), ("c_cache", _vp), ("kr_cache", _vp), ("scales", _vp), ("q", _vp), ("w_ukv", _vp),
+        ("rope_cos", _vp), ("rope_sin", _vp), ("lam_logits", _vp), ("gate_logits", _vp), ("out", _vp),
+        ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t)]
+
+
 class GatesArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("B", "L", "d_q", "d_x", "n_signal", "d_v")] + [
         ("dtype", ctypes.c_int), ("rms_eps", ctypes.c_float),
@@ -68,7 +92,9 @@ EXPORTED = ("gdla_latent_expand", "gdla_prefill_workspace_size", "gdla_prefill",
             "gdla_prefill_host", "gdla_attend", "gdla_decode_workspace_size", "gdla_decode", "gdla_decode_noalloc",
             "gdla_gates_workspace_size", "gdla_gates", "gdla_status_string", "gdla_workspace_status",
             "gdla_build_info", "gdla_diag_wait_timeout", "gdla_rope_tables", "gdla_yarn_rope_tables",
-            "gdla_yarn_mscale")
+            "gdla_yarn_mscale",
+            "gdla_qcache_scale_blocks", "gdla_qcache_write", "gdla_qcache_read", "gdla_qcache_expand",
+            "gdla_qcache_decode_workspace_size", "gdla_qcache_decode")
 
 _lock = threading.Lock()
 _lib = None
@@ -107,6 +133,18 @@ def load(path: str = LIB_PATH):
         lib.gdla_gates_workspace_size.restype = ctypes.c_size_t
         lib.gdla_gates.argtypes = [ctypes.POINTER(GatesArgs), _vp]
         lib.gdla_gates.restype = ctypes.c_int
+        lib.gdla_qcache_scale_blocks.argtypes = [ctypes.c_int, ctypes.c_int]
+        lib.gdla_qcache_scale_blocks.restype = ctypes.c_int
+        lib.gdla_qcache_write.argtypes = [ctypes.POINTER(QcacheWriteArgs), _vp]
+        lib.gdla_qcache_write.restype = ctypes.c_int
+        lib.gdla_qcache_read.argtypes = [ctypes.POINTER(QcacheReadArgs), _vp]
+        lib.gdla_qcache_read.restype = ctypes.c_int
+        lib.gdla_qcache_expand.argtypes = [ctypes.POINTER(QcacheReadArgs), _vp]
+        lib.gdla_qcache_expand.restype = ctypes.c_int
+        lib.gdla_qcache_decode_workspace_size.argtypes = [ctypes.POINTER(QcacheDecodeArgs)]
+        lib.gdla_qcache_decode_workspace_size.restype = ctypes.c_size_t
+        lib.gdla_qcache_decode.argtypes = [ctypes.POINTER(QcacheDecodeArgs), _vp]
+        lib.gdla_qcache_decode.restype = ctypes.c_int
         lib.gdla_status_string.argtypes = [ctypes.c_int]
         lib.gdla_status_string.restype = ctypes.c_char_p
         lib.gdla_workspace_status.argtypes = [_vp, _vp]

@@ -289,6 +289,20 @@ gdla_status validate_decode(const gdla_decode_args* a) {
   return GDLA_OK;
 }
 
+// log2 of a scale block's tokens; -1 where it is not a power of two in 1 .. 128
+int qcache_sl(int scale_block) {
+  for (int l = 0; l <= 7; ++l)
+    if (scale_block == 1 << l) return l;
+  return -1;
+}
+
+gdla_status qcache_dims(int B, int T_max, int d_c, int d_rope, int scale_block, int dtype) {
+  if (B < 1 || B > 65535 || T_max < 1 || qcache_sl(scale_block) < 0) return GDLA_ERR_INVALID_ARG;
+  if (dtype != GDLA_BF16 && dtype != GDLA_FP32) return GDLA_ERR_INVALID_ARG;
+  if (!latent_ok(d_c) || (d_rope != 16 && d_rope != 32 && d_rope != 64)) return GDLA_ERR_UNSUPPORTED;
+  return GDLA_OK;
+}
+
 float default_scale(float s, int d_nope, int d_rope) {
   return s > 0.f ? s : 1.0f / sqrtf((float)(d_nope + d_rope));
 }
@@ -690,6 +704,177 @@ gdla_status gdla_gates(const gdla_gates_args* a, void* stream) {
             ? (tensor_maps_available() ? launch_gemm_tc_f32out(lp, status, s) : cudaErrorNotSupported)
             : launch_gemm_simt_f32out(lp, a->dtype, s);
   }
+  return cuda_status(e);
+}
+
+// ------------------------------------------------------------ 8-bit latent cache
+int gdla_qcache_scale_blocks(int T_max, int scale_block) {
+  if (T_max < 1 || qcache_sl(scale_block) < 0) return 0;
+  return (int)(((long)T_max + scale_block - 1) / scale_block);
+}
+
+gdla_status gdla_qcache_write(const gdla_qcache_write_args* a, void* stream) {
+  if (!a) return GDLA_ERR_INVALID_ARG;
+  gdla_status st = qcache_dims(a->B, a->T_max, a->d_c, a->d_rope, a->scale_block, a->dtype);
+  if (st != GDLA_OK) return st;
+  if (a->L < 1 || a->L > a->T_max) return GDLA_ERR_INVALID_ARG;
+  const void* req[] = {a->c_kv, a->k_rope, a->c_cache, a->kr_cache, a->scales, a->workspace};
+  for (const void* p : req)
+    if (!aligned16(p)) return GDLA_ERR_INVALID_ARG;
+  if (a->gamma) {
+    if (a->rope_max_pos < a->T_max) return GDLA_ERR_INVALID_ARG;
+    if (!aligned16(a->gamma) || !aligned16(a->rope_cos) || !aligned16(a->rope_sin)) return GDLA_ERR_INVALID_ARG;
+  }
+  if (((uintptr_t)a->start & 3) != 0 || ((uintptr_t)a->lens & 3) != 0) return GDLA_ERR_INVALID_ARG;
+  if (((uintptr_t)a->workspace & 255) != 0 || a->workspace_bytes < kStatusBytes) return GDLA_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  QcacheWriteParams p{};
+  p.B = a->B; p.L = a->L; p.T_max = a->T_max; p.d_c = a->d_c; p.d_rope = a->d_rope;
+  p.sl = qcache_sl(a->scale_block); p.n_blocks = gdla_qcache_scale_blocks(a->T_max, a->scale_block);
+  p.eps = a->rms_eps > 0.f ? a->rms_eps : 1e-6f;
+  p.c_kv = a->c_kv; p.gamma = a->gamma; p.k_rope = a->k_rope; p.cos_tab = a->rope_cos; p.sin_tab = a->rope_sin;
+  p.start = a->start; p.lens = a->lens;
+  p.c8 = (uint8_t*)a->c_cache; p.kr8 = (uint8_t*)a->kr_cache; p.scales = a->scales; p.status = (int*)a->workspace;
+  return cuda_status(launch_qcache_write(p, a->dtype, s));  // (which sets the status word too)
+}
+
+static gdla_status validate_qcache_read(const gdla_qcache_read_args* a) {
+  if (!a) return GDLA_ERR_INVALID_ARG;
+  gdla_status st = qcache_dims(a->B, a->T_max, a->d_c, a->d_rope, a->scale_block, a->dtype);
+  if (st != GDLA_OK) return st;
+  if (a->L < 1 || a->first < 0 || (long)a->first + a->L > a->T_max) return GDLA_ERR_INVALID_ARG;
+  const void* req[] = {a->c_cache, a->kr_cache, a->scales, a->c_hat_out, a->k_rope_out};
+  for (const void* p : req)
+    if (!aligned16(p)) return GDLA_ERR_INVALID_ARG;
+  if (((uintptr_t)a->lens & 3) != 0) return GDLA_ERR_INVALID_ARG;
+  return GDLA_OK;
+}
+
+static cudaError_t qcache_read_rows(const gdla_qcache_read_args* a, cudaStream_t s) {
+  QcacheReadParams p{};
+  p.B = a->B; p.L = a->L; p.T_max = a->T_max; p.first = a->first; p.d_c = a->d_c; p.d_rope = a->d_rope;
+  p.sl = qcache_sl(a->scale_block); p.n_blocks = gdla_qcache_scale_blocks(a->T_max, a->scale_block);
+  p.c8 = (const uint8_t*)a->c_cache; p.kr8 = (const uint8_t*)a->kr_cache; p.scales = a->scales; p.lens = a->lens;
+  p.c_hat = a->c_hat_out; p.k_rope = a->k_rope_out;
+  return launch_qcache_read(p, a->dtype, s);
+}
+
+gdla_status gdla_qcache_read(const gdla_qcache_read_args* a, void* stream) {
+  gdla_status st = validate_qcache_read(a);
+  if (st != GDLA_OK) return st;
+  return cuda_status(qcache_read_rows(a, (cudaStream_t)stream));
+}
+
+gdla_status gdla_qcache_expand(const gdla_qcache_read_args* a, void* stream) {
+  gdla_status st = validate_qcache_read(a);
+  if (st != GDLA_OK) return st;
+  st = common_dims(a->B, a->L, a->d_c, a->d_rope, a->n_kv, a->d_nope, a->d_v, a->n_kv, 1, a->dtype);
+  if (st != GDLA_OK) return st;
+  if (!aligned16(a->w_ukv) || !aligned16(a->kv_out)) return GDLA_ERR_INVALID_ARG;
+  cudaStream_t s = (cudaStream_t)stream;
+  GemmParams gp{(long)a->B * a->L, a->n_kv * (a->d_nope + a->d_v), a->d_c, a->c_hat_out, a->w_ukv, a->kv_out};
+  const bool tc = a->dtype == GDLA_BF16 && gemm_tc_shape(gp);
+  if (tc && !tensor_maps_available()) return GDLA_ERR_CUDA;
+  cudaError_t e = qcache_read_rows(a, s);
+  if (e == cudaSuccess) e = tc ? launch_gemm_tc(gp, nullptr, s) : launch_gemm_simt(gp, a->dtype, s);
+  return cuda_status(e);
+}
+
+// The decode of the same shapes over a bf16 / fp32 cache: its dimension checks, and the layout
+// of the CUDA-core path, which the 8-bit cache's shares.
+static gdla_decode_args qdecode_shape(const gdla_qcache_decode_args* a) {
+  gdla_decode_args d{};
+  d.B = a->B; d.T_max = a->T_max; d.d_c = a->d_c; d.d_rope = a->d_rope; d.n_kv = a->n_kv; d.d_nope = a->d_nope;
+  d.d_v = a->d_v; d.n_noise = a->n_noise; d.g = a->g; d.dtype = a->dtype;
+  return d;
+}
+
+static DecodeLayout qdecode_layout(const gdla_qcache_decode_args* a) {
+  const gdla_decode_args shape = qdecode_shape(a);
+  if (!decode_uses_tc(&shape)) return decode_layout(&shape);
+  DecodeLayout l{};
+  l.tc = 1;
+  const int H_q = a->n_kv * (a->g + 1);
+  l.n_hg = (H_q + kQdecHeads - 1) / kQdecHeads;
+  l.hpc = (H_q + l.n_hg - 1) / l.n_hg;
+  l.n_hg = (H_q + l.hpc - 1) / l.hpc;  // (thousands of heads: no group is left empty)
+  l.part_heads = kQdecHeads;
+  const long tiles_max = (long)a->B * (((long)a->T_max + kQdecTile - 1) / kQdecTile);
+  l.n_ranges = (int)std::min((long)std::max(1, kQdecSMs / l.n_hg), tiles_max);
+  const size_t records = ((size_t)l.n_ranges + a->B) * l.n_hg;
+  size_t off = kStatusBytes;
+  l.qimg = off;
+  off = align256(off + (size_t)a->B * l.n_hg * kQdecImageBytes);
+  l.seqinfo = off;
+  off = align256(off + sizeof(int2) * (size_t)a->B);
+  l.part_o = off;
+  off = align256(off + sizeof(float) * records * l.part_heads * a->d_c);
+  l.part_ml = off;
+  off = align256(off + sizeof(float) * records * l.part_heads * 2);
+  l.total = off;
+  return l;
+}
+
+static gdla_status validate_qdecode(const gdla_qcache_decode_args* a) {
+  if (!a) return GDLA_ERR_INVALID_ARG;
+  gdla_status st = common_dims(a->B, a->T_max, a->d_c, a->d_rope, a->n_kv, a->d_nope, a->d_v, a->n_noise, a->g,
+                               a->dtype);
+  if (st != GDLA_OK) return st;
+  if (qcache_sl(a->scale_block) < 0) return GDLA_ERR_INVALID_ARG;
+  const gdla_decode_args shape = qdecode_shape(a);
+  // (the tensor-core path's heads are 128 wide: d_rope = 64 admits no others.) The CUDA-core
+  // split kernel holds every query head of a sequence in one block
+  if (!decode_uses_tc(&shape) && (long)a->n_kv * (a->g + 1) > 64) return GDLA_ERR_UNSUPPORTED;
+  if (a->mask != GDLA_MASK_CAUSAL && a->mask != GDLA_MASK_SLIDING) return GDLA_ERR_INVALID_ARG;
+  if (a->mask == GDLA_MASK_SLIDING && a->window < 1) return GDLA_ERR_INVALID_ARG;
+  if (a->rope_max_pos < a->T_max) return GDLA_ERR_INVALID_ARG;
+  return GDLA_OK;
+}
+
+size_t gdla_qcache_decode_workspace_size(const gdla_qcache_decode_args* a) {
+  if (!a || a->B < 1 || a->T_max < 1 || a->n_kv < 1 || a->g < 1) return 0;
+  return qdecode_layout(a).total;
+}
+
+gdla_status gdla_qcache_decode(const gdla_qcache_decode_args* a, void* stream) {
+  gdla_status st = validate_qdecode(a);
+  if (st != GDLA_OK) return st;
+  const void* req[] = {a->seqlens, a->c_cache, a->kr_cache, a->scales, a->q, a->w_ukv, a->rope_cos, a->rope_sin,
+                       a->lam_logits, a->gate_logits, a->out, a->workspace};
+  for (const void* p : req)
+    if (!aligned16(p)) return GDLA_ERR_INVALID_ARG;
+  if (((uintptr_t)a->workspace & 255) != 0) return GDLA_ERR_INVALID_ARG;
+  const DecodeLayout lay = qdecode_layout(a);
+  if (a->workspace_bytes < lay.total) return GDLA_ERR_INVALID_ARG;
+  if (lay.tc && !tensor_maps_available()) return GDLA_ERR_CUDA;
+  cudaStream_t s = (cudaStream_t)stream;
+  char* ws = (char*)a->workspace;
+  QdecodeParams p{};
+  DecodeParams& d = p.d;
+  d.B = a->B; d.T_max = a->T_max; d.d_c = a->d_c; d.d_rope = a->d_rope; d.n_kv = a->n_kv; d.g = a->g;
+  d.d_nope = a->d_nope; d.d_v = a->d_v; d.sliding = a->mask == GDLA_MASK_SLIDING;
+  d.window = d.sliding ? a->window : 0; d.rope_max_pos = a->rope_max_pos;
+  d.scale = default_scale(a->softmax_scale, a->d_nope, a->d_rope);
+  d.tc = lay.tc; d.n_splits = lay.n_splits; d.split_len = lay.split_len; d.n_ranges = lay.n_ranges;
+  d.n_hg = lay.n_hg; d.hpc = lay.hpc; d.part_heads = lay.part_heads;
+  d.seqlens = a->seqlens; d.c_cache = a->c_cache; d.kr_cache = a->kr_cache; d.q = a->q; d.w_ukv = a->w_ukv;
+  d.cos_tab = a->rope_cos; d.sin_tab = a->rope_sin; d.lam = a->lam_logits; d.gate = a->gate_logits; d.out = a->out;
+  if (lay.tc) {
+    d.qimg = (uint8_t*)(ws + lay.qimg);
+    d.seqinfo = (int2*)(ws + lay.seqinfo);
+  } else {
+    d.q_abs = (float*)(ws + lay.q_abs);
+    d.q_rot = (float*)(ws + lay.q_rot);
+  }
+  d.part_o = (float*)(ws + lay.part_o); d.part_ml = (float*)(ws + lay.part_ml);
+  d.status = (int*)(ws + lay.status);
+  p.scales = a->scales; p.sl = qcache_sl(a->scale_block);
+  p.n_blocks = gdla_qcache_scale_blocks(a->T_max, a->scale_block);
+  cudaError_t e = cudaMemsetAsync(d.status, 0, kStatusBytes, s);
+  if (e == cudaSuccess && lay.tc) return cuda_status(launch_qdecode_tc(p, s));
+  if (e == cudaSuccess) e = launch_decode_absorb(d, a->dtype, s);
+  if (e == cudaSuccess) e = launch_qdecode_split_simt(p, s);
+  if (e == cudaSuccess) e = launch_decode_combine(d, a->dtype, s);
   return cuda_status(e);
 }
 

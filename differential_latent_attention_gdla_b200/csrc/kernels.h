@@ -117,6 +117,45 @@ cudaError_t launch_decode_combine_tc(const DecodeParams& p, cudaStream_t s);
 // after absorb, whose tail it overlaps through programmatic dependent launch
 cudaError_t launch_decode_split_tc(const DecodeParams& p, cudaStream_t s);
 
+// ---- 8-bit latent cache: e4m3 rows, one fp32 scale per block of 2^sl tokens
+constexpr int kQcacheMinExp = -40;  // the smallest scale that a write sets is 2^-40
+struct QcacheWriteParams {
+  int B, L, T_max, d_c, d_rope, sl, n_blocks;
+  float eps;
+  const void* c_kv; const void* gamma; const void* k_rope;  // gamma == nullptr: rows as they are
+  const float* cos_tab; const float* sin_tab;
+  const int* start; const int* lens;
+  uint8_t* c8; uint8_t* kr8; float* scales;
+  int* status;
+};
+cudaError_t launch_qcache_write(const QcacheWriteParams& p, gdla_dtype dt, cudaStream_t s);
+struct QcacheReadParams {
+  int B, L, T_max, first, d_c, d_rope, sl, n_blocks;
+  const uint8_t* c8; const uint8_t* kr8; const float* scales;
+  const int* lens;
+  void* c_hat; void* k_rope;
+};
+cudaError_t launch_qcache_read(const QcacheReadParams& p, gdla_dtype dt, cudaStream_t s);
+
+// ---- decode over the 8-bit cache. `d` as for the bf16 cache (c_cache and kr_cache are the
+// e4m3 rows); on the tensor-core path the head groups, ranges, records and images are this
+// path's own: at most kQdecHeads heads a group, kQdecTile tokens a tile, images of
+// kQdecImageBytes (hi and lo e4m3 rows of each head, then the heads' scales).
+constexpr int kQdecHeads = 48;
+constexpr int kQdecTile = 128;
+constexpr int kQdecPrefetch = 2;  // tiles prefetched into L2 ahead of the ring
+constexpr int kQdecSMs = 148;     // B200
+constexpr int kQdecImageData = 2 * kQdecHeads * 576;
+constexpr int kQdecImageBytes = (kQdecImageData + 4 * kQdecHeads + 255) / 256 * 256;
+struct QdecodeParams {
+  DecodeParams d;
+  const float* scales;
+  int sl, n_blocks;
+};
+cudaError_t launch_qdecode_split_simt(const QdecodeParams& p, cudaStream_t s);
+// absorb, split and combine (bf16, d_c = 512, d_rope = 64, heads of 128)
+cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s);
+
 // Whether the driver's tensor-map encoder could be resolved. Every tensor-core
 // kernel needs it; a call whose shape selects one fails (GDLA_ERR_CUDA) without it
 // instead of running a CUDA-core substitute.

@@ -1,0 +1,1140 @@
+// qdecode_tc.cu -- split-KV GDLA decode over the 8-bit latent cache on the 5th-generation
+// tensor cores. A cached row is 512 + 64 e4m3 values times a scale s_j (one per block of
+// tokens), and both products of the attention run on it as it is stored:
+//   S_hj = s_j (q~_h . row8_j)            q~ = tau log2e [W_UK q_nope | RoPE(q_rope)]
+//   O_h  = sum_j 2^(S_hj) s_j c8_j        (over the sum of 2^(S_hj))
+//   S^T[tokens x heads] = row8[tokens x 576] . q8^T                (M = 128, N = 96)
+//   O^T[512 x heads]   += c8^T[512 x tokens] . w8^T[tokens x heads]  (M = 4 x 128, N = 48)
+// The tensor cores take 8-bit operands on both sides, so the other operand of each product
+// is split into two 8-bit terms, which cost no precision against a bf16 operand:
+//   * q~ / 2^k = hi + lo / 16, both e4m3 (4 + 4 significant bits and the sign of the
+//     remainder; relative rounding 6e-4 rms, bf16's is 1.6e-3): 48 heads take 96 columns
+//     of one MMA, and the softmax adds the two halves;
+//   * w = 2^(S - M) s_j = hi + lo, hi in e4m3 and lo in e5m2, whose larger exponent range
+//     holds the remainder without a scale of its own: two MMAs into one accumulator. With
+//     w <= 430 the smallest remainder kept is 2^-17, 2^-23 of the largest weight.
+// A scale enters twice, both times outside the products: it multiplies the score, and it
+// is part of the weight (the reference M is the running maximum of S + log2 s).
+//
+// Split: the visible 128-token tiles of all sequences are numbered in sequence order, and
+// CTA r of a head group takes tiles [r W / R, (r + 1) W / R): equal shares, no tail wave.
+// A share writes one partial (M, l, O) per sequence it touches, to record r + b; the
+// combine kernel merges the records of a sequence.
+//
+// Block: 384 threads. Warp 0 loads tiles (TMA, two stages of 72 KB, L2 prefetch ahead);
+// warp 1 issues the score MMAs, warp 2 the value MMAs, warp 3 loads query images; warps
+// 4-11 are the softmax: a thread owns one token (TMEM lane) and 24 heads. Every wait is
+// bounded and reports GDLA_ERR_TIMEOUT.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include "kernels.h"
+#include "sm100.cuh"
+
+namespace gdla {
+namespace q8 {
+
+constexpr int DC = 512, DR = 64;
+constexpr int TT = kQdecTile;                    // cache tokens per tile (M of the score MMA)
+constexpr int NH = kQdecHeads;                   // query heads per CTA
+constexpr int NQ = 2 * NH;                       // hi and lo rows of the query operand
+constexpr int HT = NH / 2;                       // heads per softmax thread
+constexpr int BOX = TT * 128, RBOX = TT * 64;    // a 128-column box of the tile; the rotary box
+constexpr int TILE = 4 * BOX + RBOX;
+constexpr int QBOX = NQ * 128, QRBOX = NQ * 64;  // the same of the query image
+constexpr int QIMG = 4 * QBOX + QRBOX;           // followed in memory by the NH head scales
+constexpr int STAGES = 2;
+constexpr int PPART = TT * 64;                   // weights: TT tokens x 64 heads, one byte (hi; then lo)
+constexpr int OFF_TILES = QIMG;
+constexpr int OFF_P = OFF_TILES + STAGES * TILE;
+constexpr int OFF_SH = OFF_P + 2 * PPART;
+constexpr int NSW = 8;                           // softmax warps
+constexpr int NT = 32 * (4 + NSW);
+constexpr uint32_t COL_S = 0;                    // S^T of tile k at COL_S + NQ (k & 1)
+constexpr uint32_t COL_O = 2 * NQ;               // O^T M-tile mt at COL_O + NH mt
+constexpr float kBase = 6.f;                     // weights are 2^(S + log2 s - M + kBase)
+constexpr float kThr = 2.75f;                    // M moves when exceeded by this: w <= 2^8.75 < 448
+constexpr float kMinScale = 8.6736174e-19f;      // 2^-60: keeps 1/s finite whatever the scales hold
+static_assert(QIMG == kQdecImageData && QIMG % 1024 == 0 && TILE % 1024 == 0, "1024-byte swizzle atoms");
+static_assert(NQ % 16 == 0 && NH % 16 == 0 && HT == 24, "MMA N; 24 = a 16- and an 8-column TMEM load");
+static_assert(COL_O + 4 * NH <= 512, "TMEM columns");
+
+struct Shared {
+  uint64_t full[STAGES], empty[STAGES];
+  uint64_t s_full[2], s_free[2], p_full, p_free;
+  uint64_t q_full, q_free, seg_done, mma_done;
+  uint32_t tmem_slot;
+  int abort_flag;
+  int b0;
+  int R;
+  long long p0, start, end, W;
+  long long red[NT / 32];
+  float2 tab[NH];  // per head: scale of the query, M - kBase
+  float wmax[4][NH];
+  float alpha[NH];
+};
+constexpr int SMEM = OFF_SH + (int)sizeof(Shared);
+static_assert(SMEM <= 232448, "shared memory of one CTA");
+
+struct Args {
+  int B, T_max, sliding, window, H_q, n_hg, hpc, n_ranges, sl, n_blocks;
+  const int* seqlens;
+  const uint8_t* c8;
+  const uint8_t* kr8;
+  const float* scales;
+  const uint8_t* qimg;
+  int2* seqinfo;
+  float* part_o;   // [records][NH][512]
+  float* part_ml;  // [records][NH][2]
+  int* status;
+};
+
+// the visible tiles of a sequence: tokens [lo, Tb), tiles jt0 .. jt0 + n - 1
+struct SeqTiles {
+  int Tb, lo, jt0, n;
+};
+__device__ __forceinline__ SeqTiles seq_tiles(const Args& a, int b) {
+  SeqTiles s;
+  s.Tb = min(max(__ldg(a.seqlens + b), 0), a.T_max);
+  s.lo = a.sliding ? max(0, s.Tb - a.window) : 0;
+  s.jt0 = s.lo / TT;
+  s.n = (s.Tb + TT - 1) / TT - s.jt0;
+  return s;
+}
+struct Walker {
+  const Args* a;
+  int b;
+  long long pb;  // global index of sequence b's first tile
+  SeqTiles st;
+  __device__ void init(const Args& args, int b0, long long p0) {
+    a = &args;
+    b = b0;
+    pb = p0;
+    st = seq_tiles(args, b0);
+  }
+  __device__ void seek(long long t) {  // (t never decreases)
+    while (t >= pb + st.n) {
+      pb += st.n;
+      ++b;
+      st = seq_tiles(*a, b);
+    }
+  }
+  __device__ int token0(long long t) const { return (st.jt0 + (int)(t - pb)) * TT; }
+};
+// the share that holds global tile t: the largest r with floor(r W / R) <= t
+__device__ __forceinline__ int range_of(long long t, long long W, int R) {
+  return (int)(((t + 1) * (long long)R - 1) / W);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t two) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+  return *reinterpret_cast<const __half2*>(&h);
+}
+// two weights as hi (e4m3) and lo (e5m2) pairs. The remainder is formed in fp16, whose 11 bits
+// hold the 4 of hi and more than the 3 of lo
+__device__ __forceinline__ void split_weights(float w0, float w1, uint32_t& hi, uint32_t& lo) {
+  const __half2 w = __floats2half2_rn(w0, w1);
+  hi = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&w), __NV_SATFINITE, __NV_E4M3);
+  const __half2 r = __hsub2(w, e4m3x2_to_half2(hi));
+  lo = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&r), __NV_SATFINITE, __NV_E5M2);
+}
+__device__ __forceinline__ bool bar_or(bool pred) { return sm100::named_bar_or(1, 32 * NSW, pred); }
+__device__ __forceinline__ void bar_sync() { sm100::named_bar_sync(1, 32 * NSW); }
+// 24 consecutive TMEM columns
+__device__ __forceinline__ void tmem_ld24(uint32_t t, uint32_t (&r)[HT]) {
+  sm100::tmem_ld16(t, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
+  sm100::tmem_ld8(t + 16, *reinterpret_cast<uint32_t(*)[8]>(&r[16]));
+}
+
+}  // namespace q8
+
+__global__ void __launch_bounds__(q8::NT, 1)
+    qdecode_split_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR,
+                         const q8::Args a) {
+  using namespace sm100;
+  using namespace q8;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* qs = smem;                  // query image: 4 boxes of [96 x 128 B], one of [96 x 64 B]
+  uint8_t* tiles = smem + OFF_TILES;   // stages: 4 boxes of [128 tokens x 128 B], one of [128 x 64 B]
+  uint8_t* ps = smem + OFF_P;          // weights [128 tokens x 64 B]: hi, lo
+  Shared& sh = *reinterpret_cast<Shared*>(smem + OFF_SH);
+  volatile int& abort_flag = sh.abort_flag;
+
+  grid_dep_launch();
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int hg = blockIdx.x, r = blockIdx.y;
+  if (smem_u32(smem) & 1023u) {  // the swizzled operands need it: report instead of computing garbage
+    if (tid == 0) {
+      atomicCAS(a.status, 0, (int)GDLA_ERR_CUDA);
+      atomicCAS(a.status + 1, 0, 599);
+    }
+    grid_dep_wait();
+    return;
+  }
+  if (earlier_failure(a.status)) {
+    grid_dep_wait();
+    return;
+  }
+
+  // ---- this CTA's share of the W tiles, and the sequence that holds its first tile
+  {
+    long long loc = 0;
+    for (int b = tid; b < a.B; b += NT) {
+      const int raw = __ldg(a.seqlens + b);
+      if ((raw < 0 || raw > a.T_max) && r == 0 && hg == 0) atomicCAS(a.status, 0, (int)GDLA_ERR_INVALID_ARG);
+      loc += seq_tiles(a, b).n;
+    }
+    for (int o = 16; o; o >>= 1) loc += __shfl_xor_sync(0xffffffffu, loc, o);
+    if (lane == 0) sh.red[warp] = loc;
+    __syncthreads();
+    if (tid == 0) {
+      long long W = 0;
+      for (int w = 0; w < NT / 32; ++w) W += sh.red[w];
+      const long long R = min((long long)a.n_ranges, W);
+      sh.start = r < R ? (long long)r * W / R : 0;
+      sh.end = r < R ? (long long)(r + 1) * W / R : 0;
+      sh.R = (int)R;
+      sh.b0 = -1;
+      sh.W = W;
+    }
+    __syncthreads();
+    const long long start = sh.start;
+    if (start < sh.end) {
+      long long base = 0;
+      for (int c0 = 0; c0 < a.B; c0 += NT) {
+        const int b = c0 + tid;
+        const long long n = b < a.B ? seq_tiles(a, b).n : 0;
+        long long incl = n;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        if (lane == 31) sh.red[warp] = incl;
+        __syncthreads();
+        long long wbase = base;
+        for (int w = 0; w < warp; ++w) wbase += sh.red[w];
+        long long total = 0;
+        for (int w = 0; w < NT / 32; ++w) total += sh.red[w];
+        const long long p = wbase + incl - n;
+        if (b < a.B && n > 0 && p <= start && start < p + n) {
+          sh.b0 = b;
+          sh.p0 = p;
+        }
+        base += total;
+        __syncthreads();
+        if (sh.b0 >= 0) break;
+      }
+    }
+  }
+  const long long start = sh.start, end = sh.end, W = sh.W;
+  const int R = sh.R;
+  if (start >= end || sh.b0 < 0) {  // a range beyond the tiles
+    grid_dep_wait();                // (this grid never completes before the one it overlaps)
+    return;
+  }
+  const int b0 = sh.b0;
+  const long long p0 = sh.p0;
+  const int n_tiles = (int)(end - start);
+  const int nh = min(a.hpc, a.H_q - hg * a.hpc);  // query heads of this head group
+
+  if (tid == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.s_full[i]), 1);
+      mbar_init(smem_u32(&sh.s_free[i]), NSW);
+    }
+    mbar_init(smem_u32(&sh.p_full), NSW);
+    mbar_init(smem_u32(&sh.p_free), 1);
+    mbar_init(smem_u32(&sh.q_full), 1);
+    mbar_init(smem_u32(&sh.q_free), 1);
+    mbar_init(smem_u32(&sh.seg_done), 1);
+    mbar_init(smem_u32(&sh.mma_done), 2);
+    fence_mbar_init();
+    abort_flag = 0;
+    prefetch_tmap(&tmC);
+    prefetch_tmap(&tmR);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&sh.tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem_slot;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      Walker wl, wp;  // the ring loads, and the L2 prefetches kQdecPrefetch tiles ahead of them
+      wl.init(a, b0, p0);
+      wp.init(a, b0, p0);
+      auto prefetch = [&](long long t) {
+        wp.seek(t);
+        const int j = wp.token0(t), rows = min(TT, a.T_max - j);
+        const long long row0 = (long long)wp.b * a.T_max + j;
+        bulk_prefetch_l2(a.c8 + row0 * DC, (uint32_t)rows * DC);
+        bulk_prefetch_l2(a.kr8 + row0 * DR, (uint32_t)rows * DR);
+      };
+      for (int k = STAGES; k < STAGES + kQdecPrefetch && k < n_tiles; ++k) prefetch(start + k);
+      int k = 0;
+      for (; k < n_tiles && !abort_flag; ++k) {
+        const int st = k % STAGES;
+        if (k >= STAGES) {
+          if (k + kQdecPrefetch < n_tiles) prefetch(start + k + kQdecPrefetch);
+          if (!mbar_wait(smem_u32(&sh.empty[st]), ((k / STAGES) & 1) ^ 1, a.status, 501, &abort_flag)) {
+            abort_flag = 1;
+            break;
+          }
+        }
+        const long long t = start + k;
+        wl.seek(t);
+        if (t == wl.pb && hg == 0)  // this CTA holds the sequence's first tile: record who covers it
+          a.seqinfo[wl.b] = make_int2(r, range_of(wl.pb + wl.st.n - 1, W, R));
+        const int j0 = wl.token0(t);
+        const uint32_t bar = smem_u32(&sh.full[st]);
+        const uint32_t dst = smem_u32(tiles + st * TILE);
+        mbar_expect_tx(bar, TILE);
+        for (int bx = 0; bx < 4; ++bx) tma_load_3d(dst + bx * BOX, &tmC, bar, bx * 128, j0, wl.b);
+        tma_load_3d(dst + 4 * BOX, &tmR, bar, 0, j0, wl.b);
+      }
+      if (abort_flag)
+        for (int q = (k > STAGES ? k - STAGES : 0); q < k; ++q)
+          mbar_wait(smem_u32(&sh.full[q % STAGES]), (q / STAGES) & 1, nullptr, 0);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------------- score MMAs
+    if (lane == 0) {
+      constexpr uint32_t id = idesc_f8_f32(TT, NQ, kF8E4m3, kF8E4m3, false, false);
+      const uint64_t q128 = sdesc_sw128(smem_u32(qs), 16, 1024);
+      const uint64_t q64 = sdesc_sw64(smem_u32(qs + 4 * QBOX), 16, 512);
+      Walker w;
+      w.init(a, b0, p0);
+      int seg = -1;
+      bool ok = true;
+      for (int k = 0; k < n_tiles && ok; ++k) {
+        const long long t = start + k;
+        w.seek(t);
+        const bool first = k == 0 || t == w.pb, last = k == n_tiles - 1 || t == w.pb + w.st.n - 1;
+        if (first) ok = mbar_wait(smem_u32(&sh.q_full), ++seg & 1, a.status, 510, &abort_flag);
+        if (ok) ok = mbar_wait(smem_u32(&sh.full[k % STAGES]), (k / STAGES) & 1, a.status, 511, &abort_flag);
+        // the softmax of tile k - 2 has loaded this S^T buffer
+        if (ok && k >= 2) ok = mbar_wait(smem_u32(&sh.s_free[k & 1]), ((k >> 1) & 1) ^ 1, a.status, 512, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tb = smem_u32(tiles + (k % STAGES) * TILE);
+        const uint64_t c128 = sdesc_sw128(tb, 16, 1024), c64 = sdesc_sw64(tb + 4 * BOX, 16, 512);
+        const uint32_t d = tmem + COL_S + NQ * (k & 1);
+#pragma unroll
+        for (int kk = 0; kk < 16; ++kk) {
+          const uint32_t bx = kk >> 2, off = (kk & 3) * 32;
+          mma_f8_ss(d, c128 + ((bx * BOX + off) >> 4), q128 + ((bx * QBOX + off) >> 4), id, kk > 0);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk) mma_f8_ss(d, c64 + 2 * kk, q64 + 2 * kk, id, 1);
+        mma_commit(smem_u32(&sh.s_full[k & 1]));
+        if (last) mma_commit(smem_u32(&sh.q_free));  // the query image may be replaced
+      }
+      if (!ok) abort_flag = 1;
+      mma_commit(smem_u32(&sh.mma_done));  // every MMA issued here completes before TMEM is released
+      mbar_wait(smem_u32(&sh.mma_done), 0, nullptr, 514);
+    }
+  } else if (warp == 2) {
+    // ---------------------------------------------------------- value MMAs
+    if (lane == 0) {
+      constexpr uint32_t id_hi = idesc_f8_f32(128, NH, kF8E4m3, kF8E4m3, true, true);
+      constexpr uint32_t id_lo = idesc_f8_f32(128, NH, kF8E4m3, kF8E5m2, true, true);
+      const uint64_t w_hi = sdesc_sw64(smem_u32(ps), 64, 512), w_lo = sdesc_sw64(smem_u32(ps + PPART), 64, 512);
+      Walker w;
+      w.init(a, b0, p0);
+      bool ok = true;
+      for (int k = 0; k < n_tiles && ok; ++k) {
+        const long long t = start + k;
+        w.seek(t);
+        const bool first = k == 0 || t == w.pb, last = k == n_tiles - 1 || t == w.pb + w.st.n - 1;
+        // the weights of tile k are written; their softmax has also read the previous
+        // sequence's O^T, so a new sequence may overwrite it
+        ok = mbar_wait(smem_u32(&sh.p_full), k & 1, a.status, 513, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t c = sdesc_sw128(smem_u32(tiles + (k % STAGES) * TILE), BOX, 1024);
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt) {
+#pragma unroll
+          for (int kk = 0; kk < TT / 32; ++kk) {  // 32 tokens: 4096 bytes of a box, 2048 of the weights
+            const uint64_t ca = c + ((mt * BOX + kk * 4096) >> 4);
+            mma_f8_ss(tmem + COL_O + NH * mt, ca, w_hi + ((kk * 2048) >> 4), id_hi, (!first || kk > 0) ? 1u : 0u);
+            mma_f8_ss(tmem + COL_O + NH * mt, ca, w_lo + ((kk * 2048) >> 4), id_lo, 1u);
+          }
+        }
+        mma_commit(smem_u32(&sh.empty[k % STAGES]));
+        mma_commit(smem_u32(&sh.p_free));
+        if (last) mma_commit(smem_u32(&sh.seg_done));  // O^T holds the whole sequence share
+      }
+      if (!ok) abort_flag = 1;
+      mma_commit(smem_u32(&sh.mma_done));
+      mbar_wait(smem_u32(&sh.mma_done), 0, nullptr, 515);
+    }
+  } else if (warp == 3) {
+    // -------------------------------------------------------- query images
+    if (lane == 0) {
+      Walker w;
+      w.init(a, b0, p0);
+      bool ok = true;
+      int seg = 0;
+      grid_dep_wait();  // the absorb kernel wrote them
+      for (long long t = start; t < end && ok; ++seg) {
+        w.seek(t);
+        if (seg > 0) ok = mbar_wait(smem_u32(&sh.q_free), (seg - 1) & 1, a.status, 531, &abort_flag);
+        if (!ok) break;
+        const uint32_t bar = smem_u32(&sh.q_full);
+        mbar_expect_tx(bar, QIMG);
+        bulk_load(smem_u32(qs), a.qimg + ((long long)w.b * a.n_hg + hg) * kQdecImageBytes, QIMG, bar);
+        t = w.pb + w.st.n;  // the next sequence's first tile
+      }
+      if (!ok) abort_flag = 1;
+      if (seg > 0) mbar_wait(smem_u32(&sh.q_full), (seg - 1) & 1, nullptr, 0);  // no copy is in flight at exit
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int st_id = tid - 128;            // 0 .. 255
+    const int q4 = warp & 3, hf = (warp - 4) >> 2, hb = hf * HT;
+    const int tl = q4 * 32 + lane;          // this thread's token of the tile
+    const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    Walker w, wn;
+    w.init(a, b0, p0);
+    wn.init(a, b0, p0);
+    grid_dep_wait();
+    // the scale of this thread's token of tile t (1 where the token is not visible)
+    auto load_scale = [&](long long t) {
+      wn.seek(t);
+      const int j = wn.token0(t) + tl;
+      return j >= wn.st.lo && j < wn.st.Tb ? __ldg(a.scales + (long long)wn.b * a.n_blocks + (j >> a.sl)) : 1.f;
+    };
+    float s_next = load_scale(start);
+    float lp[HT];
+    int seg = -1;
+    bool ok = true, bad = false;
+    for (int k = 0; k < n_tiles; ++k) {
+      const long long t = start + k;
+      w.seek(t);
+      const bool first = k == 0 || t == w.pb, last = k == n_tiles - 1 || t == w.pb + w.st.n - 1;
+      const float sc = s_next;
+      if (k + 1 < n_tiles) s_next = load_scale(t + 1);
+      const int j0 = w.token0(t), j = j0 + tl;
+      const bool valid = j >= w.st.lo && j < w.st.Tb;
+      if (first) {
+        ++seg;
+        if (st_id < NH) {
+          const float* hs = reinterpret_cast<const float*>(
+              a.qimg + ((long long)w.b * a.n_hg + hg) * kQdecImageBytes + QIMG);
+          sh.tab[st_id] = make_float2(hs[st_id], -INFINITY);
+        }
+#pragma unroll
+        for (int h = 0; h < HT; ++h) lp[h] = 0.f;
+        bar_sync();
+      }
+      const float sc1 = fmaxf(sc, kMinScale), ls = __log2f(sc1), inv_s = __frcp_rn(sc1);
+      bad |= !mbar_wait(smem_u32(&sh.s_full[k & 1]), (k >> 1) & 1, a.status, 522, &abort_flag);
+      __syncwarp();
+      float dot[HT], e[HT];
+      bool exceed = false;
+      {
+        tc_fence_after();
+        uint32_t xh[HT], xl[HT];
+        const uint32_t tS = tmem + lane_base + COL_S + NQ * (k & 1) + hb;
+        tmem_ld24(tS, xh);
+        tmem_ld24(tS + NH, xl);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive_warp(smem_u32(&sh.s_free[k & 1]));
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          dot[h] = fmaf(__uint_as_float(xl[h]), 0.0625f, __uint_as_float(xh[h]));
+          const float2 tb = sh.tab[hb + h];
+          e[h] = valid ? fmaf(dot[h], tb.x * sc, ls - tb.y) : -INFINITY;
+          exceed |= e[h] > kBase + kThr;
+        }
+      }
+      if (bar_or(exceed || bad)) {
+        if (bar_or(bad)) {
+          ok = false;
+          break;
+        }
+        // some head's reference moves: the tile's maximum of S + log2 s per head
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          float v = valid ? fmaf(dot[h], sh.tab[hb + h].x * sc, ls) : -INFINITY;
+#pragma unroll
+          for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+          if (lane == 0) sh.wmax[q4][hb + h] = v;
+        }
+        bar_sync();
+        bool resc = false;
+        if (st_id < NH) {
+          const float tm = fmaxf(fmaxf(sh.wmax[0][st_id], sh.wmax[1][st_id]), fmaxf(sh.wmax[2][st_id], sh.wmax[3][st_id]));
+          const float m_old = sh.tab[st_id].y + kBase;
+          const bool up = tm > m_old + kThr;  // (also when m_old is -inf and tm is not)
+          resc = up && m_old > -INFINITY;
+          sh.alpha[st_id] = ex2_approx(up ? m_old - tm : 0.f);  // (0 from -inf)
+          if (up) sh.tab[st_id].y = tm - kBase;
+        }
+        const bool any = bar_or(resc);  // (also publishes tab and alpha)
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          const float2 tb = sh.tab[hb + h];
+          lp[h] *= sh.alpha[hb + h];
+          e[h] = valid ? fmaf(dot[h], tb.x * sc, ls - tb.y) : -INFINITY;
+        }
+        if (any) {
+          // O^T holds the tiles before k once the value MMAs of tile k - 1 have landed
+          const bool r_ok = mbar_wait(smem_u32(&sh.p_free), (k - 1) & 1, a.status, 523, &abort_flag);
+          bad |= !r_ok;
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int mt = 0; mt < 4; ++mt) {
+            uint32_t o[HT];
+            const uint32_t ta = tmem + lane_base + COL_O + NH * mt + hb;
+            tmem_ld24(ta, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < HT; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * sh.alpha[hb + h]);
+            tmem_st16(ta, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
+            tmem_st8(ta + 16, *reinterpret_cast<uint32_t(*)[8]>(&o[16]));
+          }
+          tmem_wait_st();
+        }
+      }
+      // weights of this token: hi and lo bytes of 24 heads
+      uint32_t wh[HT / 4], wl[HT / 4];
+#pragma unroll
+      for (int q = 0; q < HT / 4; ++q) {
+        float p[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          p[u] = ex2_approx(e[4 * q + u]);
+          lp[4 * q + u] = fmaf(p[u], inv_s, lp[4 * q + u]);
+        }
+        uint32_t h0, l0, h1, l1;
+        split_weights(p[0], p[1], h0, l0);
+        split_weights(p[2], p[3], h1, l1);
+        wh[q] = h0 | (h1 << 16);
+        wl[q] = l0 | (l1 << 16);
+      }
+      // a row that is not visible may hold anything: its weight is zero, but 0 x NaN is NaN
+      if (!valid) {
+        uint8_t* tb = tiles + (k % STAGES) * TILE + 2 * hf * BOX + tl * 128;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          *reinterpret_cast<uint4*>(tb + (c >> 3) * BOX + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+      }
+      // the weights of tile k - 1 have been consumed
+      if (k >= 1) bad |= !mbar_wait(smem_u32(&sh.p_free), (k - 1) & 1, a.status, 524, &abort_flag);
+      __syncwarp();
+      {
+        // token row of 64 bytes, 16-byte chunks (16 heads) swizzled by bits 1..2 of the token:
+        // heads 0..23 are chunk 0 and the first half of chunk 1, heads 24..47 the rest
+        const int sw = (tl >> 1) & 3;
+        uint8_t* row = ps + tl * 64;
+        uint8_t* full_c = row + (((hf ? 2 : 0) ^ sw) << 4);
+        uint8_t* half_c = row + ((1 ^ sw) << 4) + 8 * hf;
+        if (hf) {
+          *reinterpret_cast<uint2*>(half_c) = make_uint2(wh[0], wh[1]);
+          *reinterpret_cast<uint4*>(full_c) = make_uint4(wh[2], wh[3], wh[4], wh[5]);
+          *reinterpret_cast<uint2*>(half_c + PPART) = make_uint2(wl[0], wl[1]);
+          *reinterpret_cast<uint4*>(full_c + PPART) = make_uint4(wl[2], wl[3], wl[4], wl[5]);
+        } else {
+          *reinterpret_cast<uint4*>(full_c) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+          *reinterpret_cast<uint2*>(half_c) = make_uint2(wh[4], wh[5]);
+          *reinterpret_cast<uint4*>(full_c + PPART) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
+          *reinterpret_cast<uint2*>(half_c + PPART) = make_uint2(wl[4], wl[5]);
+        }
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive_warp(smem_u32(&sh.p_full));
+
+      if (last) {
+        // ---- partial of this sequence share: (M, l) per head and O^T
+        const bool d_ok = mbar_wait(smem_u32(&sh.seg_done), seg & 1, a.status, 525, &abort_flag);
+        if (bar_or(!d_ok || bad)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < HT; ++h) {
+          float v = lp[h];
+#pragma unroll
+          for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+          if (lane == 0) sh.wmax[q4][hb + h] = v;
+        }
+        bar_sync();
+        const long long rec = ((long long)(r + w.b) * a.n_hg + hg) * NH;
+        if (st_id < nh) {
+          a.part_ml[(rec + st_id) * 2 + 0] = sh.tab[st_id].y + kBase;
+          a.part_ml[(rec + st_id) * 2 + 1] =
+              (sh.wmax[0][st_id] + sh.wmax[1][st_id]) + (sh.wmax[2][st_id] + sh.wmax[3][st_id]);
+        }
+#pragma unroll 1
+        for (int mt = 0; mt < 4; ++mt) {
+          uint32_t o[HT];
+          tmem_ld24(tmem + lane_base + COL_O + NH * mt + hb, o);
+          tmem_wait_ld();
+          float* dst = a.part_o + (rec + hb) * DC + mt * 128 + q4 * 32 + lane;
+#pragma unroll
+          for (int h = 0; h < HT; ++h)
+            if (hb + h < nh) dst[h * DC] = __uint_as_float(o[h]);
+        }
+        tc_fence_before();
+        bar_sync();
+      }
+    }
+    if (!ok || bad) abort_flag = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+// ---------------------------------------------------------------- absorb
+// q~ = tau log2e [W_UK q_nope | RoPE(q_rope)], quantised into the split kernel's images. For
+// KV group h and 128 query rows (row = (sequence b, head u of the group)) a cluster of four
+// CTAs computes the 512 latent columns, 128 each, on the tensor cores; the largest magnitude
+// of a row is exchanged through distributed shared memory, so that the row is scaled by one
+// power of two and written once. The first CTA adds the rotary part.
+namespace q8 {
+constexpr int AB = 128;
+constexpr int AB_OP = AB * AB * 2;  // an operand: two 64-column chunks of [128 rows x 128 B]
+constexpr int AB_SMEM = 2 * AB_OP + 64;
+struct AbsorbArgs {
+  int B, T_max, n_kv, g, H_q, n_hg, hpc;
+  float isc;
+  const __nv_bfloat16* q;
+  const int* seqlens;
+  const float* cos_tab;
+  const float* sin_tab;
+  uint8_t* qimg;
+  int* status;
+};
+// byte of dimension d of image row (hi: head; lo: NH + head)
+__device__ __forceinline__ int image_offset(int row, int d) {
+  return d < DC ? (d >> 7) * QBOX + row * 128 + ((((d & 127) >> 4) ^ (row & 7)) << 4) + (d & 15)
+                : 4 * QBOX + row * 64 + ((((d - DC) >> 4) ^ ((row >> 1) & 3)) << 4) + (d & 15);
+}
+// 16 values (already divided by the row's scale) into the hi and lo rows
+__device__ __forceinline__ void store16(uint8_t* img, int head, int d, const float (&x)[16]) {
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t hh[2], ll[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float a = x[4 * q + 2 * u], b = x[4 * q + 2 * u + 1];
+      hh[u] = e4m3x2(a, b);
+      const float2 f = __half22float2(e4m3x2_to_half2(hh[u]));
+      ll[u] = e4m3x2((a - f.x) * 16.f, (b - f.y) * 16.f);
+    }
+    hi[q] = hh[0] | (hh[1] << 16);
+    lo[q] = ll[0] | (ll[1] << 16);
+  }
+  *reinterpret_cast<uint4*>(img + image_offset(head, d)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(img + image_offset(NH + head, d)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+}  // namespace q8
+
+__global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
+    qdecode_absorb_kernel(const __grid_constant__ CUtensorMap tmW, const q8::AbsorbArgs a) {
+  using namespace sm100;
+  using namespace q8;
+  grid_dep_launch();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* as = smem;
+  uint8_t* bs = smem + AB_OP;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + 2 * AB_OP);  // [0] W landed, [1] MMAs done
+  __shared__ uint32_t tmem_slot;
+  __shared__ float part_max[2][AB], row_max[AB];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int h = blockIdx.x, z = blockIdx.z;
+  const int G1 = a.g + 1, n_S = a.g * a.n_kv, rows = a.B * G1, r0 = blockIdx.y * AB;
+  // (the cluster's CTAs have the same shared-memory layout: all four or none pass this)
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) {
+      atomicCAS(a.status, 0, (int)GDLA_ERR_CUDA);
+      atomicCAS(a.status + 1, 0, 598);
+    }
+    return;
+  }
+  if (tid == 0) {
+    mbar_init(smem_u32(&bar[0]), 1);
+    mbar_init(smem_u32(&bar[1]), 1);
+    fence_mbar_init();
+    prefetch_tmap(&tmW);
+    mbar_expect_tx(smem_u32(&bar[0]), AB_OP);
+    for (int kc = 0; kc < 2; ++kc)
+      tma_load_2d(smem_u32(bs + kc * (AB_OP / 2)), &tmW, smem_u32(&bar[0]), h * 256 + kc * 64, z * AB);
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&tmem_slot), AB);
+    tmem_relinquish();
+  }
+  auto head_of = [&](int u) { return u < a.g ? h * a.g + u : n_S + h; };
+  constexpr int kPieces = AB * 16 / 256;
+  uint4 qv[kPieces];
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    const int e = tid + 256 * u, rr = e >> 4, pc = e & 15, R = r0 + rr;
+    qv[u] = make_uint4(0, 0, 0, 0);
+    if (R < rows)
+      qv[u] = *reinterpret_cast<const uint4*>(a.q + ((long long)(R / G1) * a.H_q + head_of(R % G1)) * 192 + pc * 8);
+  }
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    const int e = tid + 256 * u, rr = e >> 4, pc = e & 15;
+    *reinterpret_cast<uint4*>(as + (pc >> 3) * (AB_OP / 2) + rr * 128 + (((pc & 7) ^ (rr & 7)) << 4)) = qv[u];
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (tid == 32) {
+    if (mbar_wait(smem_u32(&bar[0]), 0, a.status, 541)) {
+      tc_fence_after();
+      constexpr uint32_t id = idesc_bf16_f32(AB, AB, false, false);
+#pragma unroll
+      for (int kk = 0; kk < AB / 16; ++kk) {
+        const uint32_t off = (uint32_t)((kk & 3) * 32);
+        mma_ss(tmem, sdesc_sw128(smem_u32(as + (kk >> 2) * (AB_OP / 2)) + off, 16, 1024),
+               sdesc_sw128(smem_u32(bs + (kk >> 2) * (AB_OP / 2)) + off, 16, 1024), id, kk > 0);
+      }
+    }
+    mma_commit(smem_u32(&bar[1]));
+  }
+  __syncwarp();
+  const int q4 = warp & 3, ch = warp >> 2;  // TMEM lane quarter; half of the 128 columns
+  const int rl = q4 * 32 + lane, R = r0 + rl;
+  const bool real = R < rows;
+  const int b = real ? R / G1 : 0, head = real ? head_of(R % G1) : 0;
+  // the rotary pairs (k, k + 32), k = 8c .. 8c + 7, at position seqlen - 1
+  const int pos = min(max(__ldg(a.seqlens + b), 1), a.T_max) - 1;
+  auto rope8 = [&](int c, float (&lo)[8], float (&hi)[8]) {
+    const __nv_bfloat16* qr = a.q + ((long long)b * a.H_q + head) * 192 + 128;
+    const uint4 xl = *reinterpret_cast<const uint4*>(qr + 8 * c);
+    const uint4 xh = *reinterpret_cast<const uint4*>(qr + 32 + 8 * c);
+    const __nv_bfloat162* l2 = reinterpret_cast<const __nv_bfloat162*>(&xl);
+    const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&xh);
+    const float* cs = a.cos_tab + (long long)pos * 32 + 8 * c;
+    const float* sn = a.sin_tab + (long long)pos * 32 + 8 * c;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 x1 = __bfloat1622float2(l2[e]), x2 = __bfloat1622float2(h2[e]);
+      lo[2 * e] = (x1.x * cs[2 * e] - x2.x * sn[2 * e]) * a.isc;
+      lo[2 * e + 1] = (x1.y * cs[2 * e + 1] - x2.y * sn[2 * e + 1]) * a.isc;
+      hi[2 * e] = (x2.x * cs[2 * e] + x1.x * sn[2 * e]) * a.isc;
+      hi[2 * e + 1] = (x2.y * cs[2 * e + 1] + x1.y * sn[2 * e + 1]) * a.isc;
+    }
+  };
+  const bool rot = z == 0 && ch == 0 && real;
+  float rmx = 0.f;
+  if (rot) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float lo[8], hi[8];
+      rope8(c, lo, hi);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) rmx = fmaxf(rmx, fmaxf(fabsf(lo[e]), fabsf(hi[e])));
+    }
+  }
+  const bool done = mbar_wait(smem_u32(&bar[1]), 0, a.status, 542);
+  __syncwarp();
+  tc_fence_after();
+  uint32_t v0[32], v1[32];
+  tmem_ld32(tmem + ((uint32_t)(q4 * 32) << 16) + ch * 64, v0);
+  tmem_ld32(tmem + ((uint32_t)(q4 * 32) << 16) + ch * 64 + 32, v1);
+  tmem_wait_ld();
+  float mx = rmx;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v0[i] = __float_as_uint(__uint_as_float(v0[i]) * a.isc);
+    v1[i] = __float_as_uint(__uint_as_float(v1[i]) * a.isc);
+    mx = fmaxf(mx, fmaxf(fabsf(__uint_as_float(v0[i])), fabsf(__uint_as_float(v1[i]))));
+  }
+  part_max[ch][rl] = mx;
+  __syncthreads();
+  if (tid < AB) row_max[tid] = fmaxf(part_max[0][tid], part_max[1][tid]);
+  cluster_sync();
+  float top = 0.f;
+#pragma unroll
+  for (uint32_t c = 0; c < 4; ++c) top = fmaxf(top, ld_shared_cluster(mapa_shared(smem_u32(&row_max[rl]), c)));
+  // the row's scale: a power of two with top <= 448 scale (448 = 1.75 2^8)
+  int ex = 0;
+  if (top > 0.f && top < INFINITY) {
+    const uint32_t u = __float_as_uint(top);
+    ex = max((int)(u >> 23) - 127 - ((u & 0x7FFFFFu) <= 0x600000u ? 8 : 7), -100);
+  }
+  const float inv = __int_as_float((127 - ex) << 23);
+  if (real && done && !earlier_failure(a.status)) {
+    const int hgi = head / a.hpc, lh = head - hgi * a.hpc;
+    uint8_t* img = a.qimg + ((long long)b * a.n_hg + hgi) * kQdecImageBytes;
+    // (an infinity would saturate: a query that is not finite gives NaN, as its scores would)
+    const float bad = top < INFINITY ? 0.f : NAN;
+    float x[16];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        x[i] = fmaf(__uint_as_float(c < 2 ? v0[16 * (c & 1) + i] : v1[16 * (c & 1) + i]), inv, bad);
+      store16(img, lh, z * AB + ch * 64 + 16 * c, x);
+    }
+    if (rot) {
+      *reinterpret_cast<float*>(img + QIMG + 4 * lh) = __int_as_float((127 + ex) << 23);
+#pragma unroll
+      for (int c2 = 0; c2 < 2; ++c2) {
+        float y[16];
+        float lo0[8], hi0[8], lo1[8], hi1[8];
+        rope8(2 * c2, lo0, hi0);
+        rope8(2 * c2 + 1, lo1, hi1);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[e] = fmaf(lo0[e], inv, bad);
+          x[8 + e] = fmaf(lo1[e], inv, bad);
+          y[e] = fmaf(hi0[e], inv, bad);
+          y[8 + e] = fmaf(hi1[e], inv, bad);
+        }
+        store16(img, lh, DC + 16 * c2, x);
+        store16(img, lh, DC + 32 + 16 * c2, y);
+      }
+    }
+  }
+  // image rows of the padding heads of each head group are zero (their scale is 1): the blocks
+  // of KV group 0 clear them for the sequences whose first row falls in their tile
+  if (h == 0 && z == 0) {
+    const int b_lo = (r0 + G1 - 1) / G1, b_hi = min(a.B, (r0 + AB + G1 - 1) / G1);
+    for (int bb = b_lo; bb < b_hi; ++bb)
+      for (int hg2 = 0; hg2 < a.n_hg; ++hg2) {
+        const int nhd = min(a.hpc, a.H_q - hg2 * a.hpc);
+        uint8_t* im = a.qimg + ((long long)bb * a.n_hg + hg2) * kQdecImageBytes;
+        for (int e = tid; e < (NH - nhd) * 72; e += 256) {
+          const int lh = nhd + e / 72, c = e % 72, part = c / 36, d = (c % 36) * 16;
+          *reinterpret_cast<uint4*>(im + image_offset(part * NH + lh, d)) = make_uint4(0, 0, 0, 0);
+          if (c == 0) *reinterpret_cast<float*>(im + QIMG + 4 * lh) = 1.f;
+        }
+      }
+  }
+  cluster_sync();  // (no CTA of the cluster leaves while another reads its row maxima)
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, AB);
+}
+
+// --------------------------------------------------------------- combine
+// Merge of the partials, W_UV product and output epilogue. Block = (KV group h, whole
+// sequences: up to 32 query rows, row = (sequence b, head u of the group)):
+//   O_lat = sum_s 2^(M_s - M) O_s / sum_s 2^(M_s - M) l_s;  H = O_lat W_UV;
+//   D = H_S - sigmoid(lambda) H_N;  Y = sigmoid(G) D.
+// The product runs on the tensor cores with O_lat as the sum of two bf16 values, rows 0..31
+// of the M = 64 operand the rounded ones and rows 32..63 what the rounding left, added in the
+// epilogue: the difference of two heads with nearly equal outputs keeps its precision.
+namespace q8 {
+constexpr int CB_R = 32, CB_N = 128;
+constexpr int CB_A = 64 * DC * 2;        // 8 chunks of [64 rows x 128 B]
+constexpr int CB_B = DC * CB_N * 2;      // 2 MN blocks of [512 K rows x 128 B]
+constexpr int CB_SMEM = CB_A + CB_B + 64;
+constexpr int CB_T = 512;
+struct CombineArgs {
+  int B, T_max, n_kv, g, H_q, n_hg, hpc, n_ranges, spb;
+  const int* seqlens;
+  const int2* seqinfo;
+  const float* part_o;
+  const float* part_ml;
+  const float* lam;
+  const __nv_bfloat16* gate;
+  __nv_bfloat16* out;
+  int* status;
+};
+}  // namespace q8
+
+__global__ void __launch_bounds__(q8::CB_T, 1)
+    qdecode_combine_kernel(const __grid_constant__ CUtensorMap tmW, const q8::CombineArgs a) {
+  using namespace sm100;
+  using namespace q8;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* as = smem;         // O_lat; later H (fp32 [64 x 128])
+  uint8_t* bs = smem + CB_A;  // W_UV,h
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + CB_A + CB_B);
+  __shared__ long long rec0[CB_R];
+  __shared__ int n_parts[CB_R];
+  __shared__ float row_max[CB_R], row_inv[CB_R];
+  __shared__ uint32_t tmem_slot;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (smem_u32(smem) & 1023u) {
+    if (tid == 0) {
+      atomicCAS(a.status, 0, (int)GDLA_ERR_CUDA);
+      atomicCAS(a.status + 1, 0, 597);
+    }
+    grid_dep_wait();
+    return;
+  }
+  const int h = blockIdx.x, G1 = a.g + 1, n_S = a.g * a.n_kv;
+  const int b0 = blockIdx.y * a.spb, nb = min(a.spb, a.B - b0), R = nb * G1;
+  const long long rstep = (long long)a.n_hg * NH;
+  if (tid == 0) {
+    mbar_init(smem_u32(&bar[0]), 1);
+    mbar_init(smem_u32(&bar[1]), 1);
+    fence_mbar_init();
+    prefetch_tmap(&tmW);
+    mbar_expect_tx(smem_u32(&bar[0]), CB_B);
+    for (int j = 0; j < 2; ++j)
+      for (int kh = 0; kh < 2; ++kh)
+        tma_load_2d(smem_u32(bs + j * (CB_B / 2) + kh * (CB_B / 4)), &tmW, smem_u32(&bar[0]), h * 256 + 128 + 64 * j,
+                    256 * kh);
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&tmem_slot), CB_N);
+    tmem_relinquish();
+  }
+  grid_dep_wait();  // the partials come from the split kernel
+  if (tid < CB_R) {
+    n_parts[tid] = 0;
+    rec0[tid] = 0;
+    if (tid < R) {
+      const int b = b0 + tid / G1, u = tid % G1, head = u < a.g ? h * a.g + u : n_S + h;
+      const int hgi = head / a.hpc, lh = head - hgi * a.hpc;
+      if (__ldg(a.seqlens + b) > 0) {
+        // first and last share of the sequence (clamped: a call whose split kernel gave up
+        // early still reads inside the records); an empty sequence has none and gives zeros
+        const int2 info = a.seqinfo[b];
+        const int x = min(max(info.x, 0), a.n_ranges - 1), y = min(max(info.y, x), a.n_ranges - 1);
+        rec0[tid] = ((long long)(x + b) * a.n_hg + hgi) * NH + lh;
+        n_parts[tid] = y - x + 1;
+      }
+    }
+  }
+  __syncthreads();
+  for (int r = warp; r < R; r += CB_T / 32) {
+    const int np = n_parts[r];
+    const long long r0 = rec0[r];
+    float M = -INFINITY;
+    for (int sp = lane; sp < np; sp += 32) M = fmaxf(M, a.part_ml[(r0 + sp * rstep) * 2]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float den = 0.f;
+    for (int sp = lane; sp < np; sp += 32) {
+      const float m = a.part_ml[(r0 + sp * rstep) * 2], l = a.part_ml[(r0 + sp * rstep) * 2 + 1];
+      // (a share whose every score was NaN has M = -inf and l = NaN, and passes it on)
+      den += m == -INFINITY ? l : exp2f(m - M) * l;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+    if (lane == 0) {
+      row_max[r] = M;
+      row_inv[r] = den == 0.f ? 0.f : 1.f / den;
+    }
+  }
+  __syncthreads();
+  constexpr int kMB = 8;  // partials in flight per thread
+  for (int e = tid; e < CB_R * (DC / 8); e += CB_T) {
+    const int r = e / (DC / 8), c8 = e % (DC / 8);
+    float acc[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[q] = 0.f;
+    if (r < R) {
+      const int np = n_parts[r];
+      const float M = row_max[r], inv = row_inv[r];
+      const float* src = a.part_o + rec0[r] * DC + c8 * 8;
+      const float* mls = a.part_ml + rec0[r] * 2;
+      for (int sp0 = 0; sp0 < np; sp0 += kMB) {
+        float4 x[kMB][2];
+        float wv[kMB];
+#pragma unroll
+        for (int q = 0; q < kMB; ++q) {
+          x[q][0] = x[q][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          wv[q] = 0.f;
+          if (sp0 + q < np) {
+            const float4* s4 = reinterpret_cast<const float4*>(src + (sp0 + q) * rstep * DC);
+            x[q][0] = s4[0];
+            x[q][1] = s4[1];
+            wv[q] = mls[(sp0 + q) * rstep * 2];
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kMB; ++q) {
+          if (sp0 + q >= np) continue;
+          const float f = wv[q] == -INFINITY ? inv : exp2f(wv[q] - M) * inv;
+          acc[0] = fmaf(f, x[q][0].x, acc[0]); acc[1] = fmaf(f, x[q][0].y, acc[1]);
+          acc[2] = fmaf(f, x[q][0].z, acc[2]); acc[3] = fmaf(f, x[q][0].w, acc[3]);
+          acc[4] = fmaf(f, x[q][1].x, acc[4]); acc[5] = fmaf(f, x[q][1].y, acc[5]);
+          acc[6] = fmaf(f, x[q][1].z, acc[6]); acc[7] = fmaf(f, x[q][1].w, acc[7]);
+        }
+      }
+    }
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      hi[q] = pack_bf16x2(acc[2 * q], acc[2 * q + 1]);
+      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&hi[q]));
+      lo[q] = pack_bf16x2(acc[2 * q] - f.x, acc[2 * q + 1] - f.y);
+    }
+    uint8_t* at = as + (c8 >> 3) * (64 * 128) + r * 128 + (((c8 & 7) ^ (r & 7)) << 4);
+    *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(at + CB_R * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  if (tid == 32) {
+    if (mbar_wait(smem_u32(&bar[0]), 0, a.status, 551)) {
+      tc_fence_after();
+      constexpr uint32_t id = idesc_bf16_f32(64, CB_N, false, true);
+#pragma unroll
+      for (int kk = 0; kk < DC / 16; ++kk)
+        mma_ss(tmem, sdesc_sw128(smem_u32(as + (kk >> 2) * (64 * 128)) + (kk & 3) * 32, 16, 1024),
+               sdesc_sw128(smem_u32(bs) + kk * 2048, CB_B / 2, 1024), id, kk > 0);
+    }
+    mma_commit(smem_u32(&bar[1]));
+  }
+  __syncwarp();
+  const bool done = mbar_wait(smem_u32(&bar[1]), 0, a.status, 552);
+  __syncwarp();
+  tc_fence_after();
+  // the M = 64 accumulator: row 16 q + l in lane l < 16 of quarter q
+  float* hs = reinterpret_cast<float*>(as);
+  {
+    const int q4 = warp & 3, c = warp >> 2;
+    uint32_t v[32];
+    tmem_ld32(tmem + ((uint32_t)(q4 * 32) << 16) + c * 32, v);
+    tmem_wait_ld();
+    if (lane < 16) {
+      float* dst = hs + (q4 * 16 + lane) * CB_N + c * 32;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        reinterpret_cast<float4*>(dst)[q] = make_float4(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                                                        __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+    }
+  }
+  __syncthreads();
+  if (done && !earlier_failure(a.status)) {
+    for (int e = tid; e < nb * a.g * (CB_N / 8); e += CB_T) {
+      const int bl = e / (a.g * (CB_N / 8)), u = (e / (CB_N / 8)) % a.g, c8 = e % (CB_N / 8);
+      const int b = b0 + bl, sh = h * a.g + u;
+      const float lamv = sigmoidf_(a.lam[(long long)b * n_S + sh]);
+      const long long idx = ((long long)b * n_S + sh) * CB_N + c8 * 8;
+      const uint4 gv = *reinterpret_cast<const uint4*>(a.gate + idx);
+      const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&gv);
+      const float* hsr = hs + (bl * G1 + u) * CB_N + c8 * 8;
+      const float* hnr = hs + (bl * G1 + a.g) * CB_N + c8 * 8;
+      uint32_t o[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float2 gf = __bfloat1622float2(g2[q]);
+        float d[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          d[i] = (hsr[2 * q + i] + hsr[CB_R * CB_N + 2 * q + i]) - lamv * (hnr[2 * q + i] + hnr[CB_R * CB_N + 2 * q + i]);
+        o[q] = pack_bf16x2(d[0] * sigmoidf_(gf.x), d[1] * sigmoidf_(gf.y));
+      }
+      *reinterpret_cast<uint4*>(a.out + idx) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, CB_N);
+}
+
+// ---------------------------------------------------------------- launches
+namespace {
+
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*k)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, args...);
+}
+
+bool w_map(CUtensorMap* m, const DecodeParams& d, uint32_t rows) {
+  const int ncol = d.n_kv * (d.d_nope + d.d_v);
+  const uint64_t dims[2] = {(uint64_t)ncol, (uint64_t)d.d_c}, str[1] = {(uint64_t)ncol * 2};
+  const uint32_t box[2] = {64, rows};
+  return make_tmap_bf16(m, d.w_ukv, 2, dims, str, box);
+}
+
+}  // namespace
+
+cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s) {
+  using namespace q8;
+  const DecodeParams& d = p.d;
+  const int H_q = d.n_kv * (d.g + 1);
+  {
+    CUtensorMap tw;
+    if (!w_map(&tw, d, AB)) return cudaErrorInvalidValue;
+    AbsorbArgs a{};
+    a.B = d.B; a.T_max = d.T_max; a.n_kv = d.n_kv; a.g = d.g; a.H_q = H_q; a.n_hg = d.n_hg; a.hpc = d.hpc;
+    a.isc = d.scale * kLog2e;
+    a.q = reinterpret_cast<const __nv_bfloat16*>(d.q); a.seqlens = d.seqlens; a.cos_tab = d.cos_tab;
+    a.sin_tab = d.sin_tab; a.qimg = d.qimg; a.status = d.status;
+    cudaError_t e = cudaFuncSetAttribute(qdecode_absorb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
+    if (e != cudaSuccess) return e;
+    const int rows = d.B * (d.g + 1);
+    qdecode_absorb_kernel<<<dim3((unsigned)d.n_kv, (unsigned)((rows + AB - 1) / AB), DC / AB), 256, AB_SMEM, s>>>(tw, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  {
+    CUtensorMap tc, tr;
+    const uint64_t cd[3] = {(uint64_t)DC, (uint64_t)d.T_max, (uint64_t)d.B};
+    const uint64_t cs[2] = {(uint64_t)DC, (uint64_t)d.T_max * DC};
+    const uint32_t cb[3] = {128, (uint32_t)TT, 1};
+    const uint64_t rd[3] = {(uint64_t)DR, (uint64_t)d.T_max, (uint64_t)d.B};
+    const uint64_t rs[2] = {(uint64_t)DR, (uint64_t)d.T_max * DR};
+    const uint32_t rb[3] = {64, (uint32_t)TT, 1};
+    if (!make_tmap_u8(&tc, d.c_cache, 3, cd, cs, cb, 128) || !make_tmap_u8(&tr, d.kr_cache, 3, rd, rs, rb, 64))
+      return cudaErrorInvalidValue;
+    Args a{};
+    a.B = d.B; a.T_max = d.T_max; a.sliding = d.sliding; a.window = d.window; a.H_q = H_q; a.n_hg = d.n_hg;
+    a.hpc = d.hpc; a.n_ranges = d.n_ranges; a.sl = p.sl; a.n_blocks = p.n_blocks; a.seqlens = d.seqlens;
+    a.c8 = (const uint8_t*)d.c_cache; a.kr8 = (const uint8_t*)d.kr_cache; a.scales = p.scales; a.qimg = d.qimg;
+    a.seqinfo = d.seqinfo; a.part_o = d.part_o; a.part_ml = d.part_ml; a.status = d.status;
+    cudaError_t e = launch_dependent(qdecode_split_kernel, dim3((unsigned)d.n_hg, (unsigned)d.n_ranges), NT, SMEM, s, tc,
+                                     tr, a);
+    if (e != cudaSuccess) return e;
+  }
+  CUtensorMap tw;
+  if (!w_map(&tw, d, 256)) return cudaErrorInvalidValue;
+  CombineArgs a{};
+  a.B = d.B; a.T_max = d.T_max; a.n_kv = d.n_kv; a.g = d.g; a.H_q = H_q; a.n_hg = d.n_hg; a.hpc = d.hpc;
+  a.n_ranges = d.n_ranges; a.seqlens = d.seqlens; a.seqinfo = d.seqinfo; a.part_o = d.part_o; a.part_ml = d.part_ml;
+  a.lam = d.lam; a.gate = reinterpret_cast<const __nv_bfloat16*>(d.gate);
+  a.out = reinterpret_cast<__nv_bfloat16*>(d.out); a.status = d.status;
+  // sequences per block: as few as fill one wave of blocks over the SMs, at most the 32 rows
+  const int per_group = kQdecSMs / d.n_kv > 1 ? kQdecSMs / d.n_kv : 1;
+  const int fill = (d.B + per_group - 1) / per_group, cap = CB_R / (d.g + 1);
+  a.spb = fill < 1 ? 1 : (fill > cap ? cap : fill);
+  return launch_dependent(qdecode_combine_kernel, dim3((unsigned)d.n_kv, (unsigned)((d.B + a.spb - 1) / a.spb)), CB_T,
+                          CB_SMEM, s, tw, a);
+}
+
+}  // namespace gdla

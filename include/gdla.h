@@ -326,6 +326,131 @@ typedef struct {
 size_t gdla_gates_workspace_size(const gdla_gates_args* args);
 gdla_status gdla_gates(const gdla_gates_args* args, void* stream);
 
+/* ------------------------------------------------------- 8-bit latent cache
+ * The decode cache in 8 bits (the report has no counterpart; it halves the bytes
+ * of the bf16 cache, which bound the decode step and the batch that fits). A
+ * cached row -- the normalised latent and the rotated rotary key of one token --
+ * is held as e4m3 values, with one fp32 scale for each block of `scale_block`
+ * consecutive tokens of a sequence (a power of two, 1 .. 128):
+ *   c_hat[b, t]  = scales[b, t / scale_block] * c_cache[b, t]
+ *   k_rope[b, t] = scales[b, t / scale_block] * kr_cache[b, t]
+ * c_cache is [B, T_max, d_c], kr_cache [B, T_max, d_rope], one byte a value, and
+ * scales [B, gdla_qcache_scale_blocks(T_max, scale_block)]. The latent cache has
+ * one head, shared by every query head, and e4m3 keeps its relative precision over
+ * 14 powers of two, so one scale serves both parts of a row.
+ *
+ * Scales must be positive and finite. gdla_qcache_write sets each to the smallest
+ * power of two (at least 2^-40) by which the block's largest magnitude is at most
+ * 448, so that rows read back as bf16 are exact and a row's rounding does not depend
+ * on its block. Rows that a call does not read or write may hold anything, NaN bit
+ * patterns included, and so may their scales.
+ *
+ * Supported: d_c in {64, 128, 256, 512}, d_rope in {16, 32, 64} for write and read;
+ * the head shapes of the other entry points for expand and decode. */
+
+/* Scales of one sequence: ceil(T_max / scale_block); 0 for an invalid size. */
+int gdla_qcache_scale_blocks(int T_max, int scale_block);
+
+/* Writes the rows of new tokens: latent RMSNorm, RoPE of the rotary key at the
+ * token's position (both as in gdla_latent_expand, kept in fp32 or more until the
+ * one rounding to 8 bits), quantisation, store. Sequence b's tokens
+ * 0 .. lens[b]-1 of the [B, L] inputs go to positions start[b] .. start[b]+lens[b]-1
+ * (a prompt, a chunk behind a cached prefix, or the single token of a decode step).
+ *  - gamma == NULL: c_kv and k_rope are rows already normalised and rotated (the
+ *    cache_c_hat and cache_k_rope outputs of gdla_prefill, for one) and are
+ *    quantised as they are; rope_cos, rope_sin, rope_max_pos and rms_eps are ignored.
+ *  - A block that the call writes from its first token on takes a new scale. A block
+ *    that already holds earlier tokens keeps its scale unless a new row needs a larger
+ *    one; then the earlier rows of the block are brought to it (exactly, but for values
+ *    that fall below e4m3's smallest normal value). Rows behind the written ones in the
+ *    last block keep their bytes, but no longer a scale of their own: a sequence is
+ *    written front to back (or, after a truncation, on from where it was cut).
+ *  - A value that is not finite is stored as NaN and takes no part in the scale.
+ *  - A sequence with start[b] < 0, lens[b] outside [0, L] or start[b] + lens[b] > T_max
+ *    is left unwritten and reported as GDLA_ERR_INVALID_ARG in the workspace status
+ *    word (the host cannot check device arrays). */
+typedef struct {
+  int B, L, T_max;           /* sequences, new tokens per sequence (at most), cache rows per sequence */
+  int d_c, d_rope, scale_block;
+  gdla_dtype dtype;          /* element type of c_kv, gamma and k_rope */
+  float rms_eps;             /* <= 0 selects 1e-6 */
+  int rope_max_pos;          /* rows of the RoPE tables; must be >= T_max */
+  const void* c_kv;          /* [B, L, d_c] pre-norm latent (normalised if gamma is NULL) */
+  const void* gamma;         /* [d_c], or NULL */
+  const void* k_rope;        /* [B, L, d_rope] pre-RoPE (rotated if gamma is NULL) */
+  const float* rope_cos;     /* [rope_max_pos, d_rope/2] */
+  const float* rope_sin;     /* [rope_max_pos, d_rope/2] */
+  const int* start;          /* [B] on the device, or NULL: 0 for every sequence */
+  const int* lens;           /* [B] on the device, or NULL: L for every sequence */
+  void* c_cache;             /* [B, T_max, d_c] e4m3 (updated) */
+  void* kr_cache;            /* [B, T_max, d_rope] e4m3 (updated) */
+  float* scales;             /* [B, ceil(T_max/scale_block)] (updated) */
+  void* workspace;           /* the status word: >= 256 bytes, 256-byte aligned */
+  size_t workspace_bytes;
+} gdla_qcache_write_args;
+
+gdla_status gdla_qcache_write(const gdla_qcache_write_args* args, void* stream);
+
+/* Reads rows first .. first+L-1 of every sequence back:
+ *   gdla_qcache_read    c_hat_out and k_rope_out;
+ *   gdla_qcache_expand  the same, and the expanded heads kv_out = c_hat W_UKV, in the
+ *                       layout of gdla_latent_expand: with first = 0 they are the key
+ *                       side of gdla_attend over a cached prefix (its q_start form),
+ *                       so a prompt can be prefilled in chunks over the 8-bit cache.
+ * Of the L rows of sequence b the first lens[b] (clamped into [0, L]) are read; the
+ * others come back as zeros. gdla_qcache_read ignores n_kv, d_nope, d_v, w_ukv and
+ * kv_out. */
+typedef struct {
+  int B, L, T_max, first;    /* first >= 0, L >= 1, first + L <= T_max */
+  int d_c, d_rope, scale_block;
+  int n_kv, d_nope, d_v;
+  gdla_dtype dtype;          /* element type of the outputs and of w_ukv */
+  const void* c_cache;       /* [B, T_max, d_c] e4m3 */
+  const void* kr_cache;      /* [B, T_max, d_rope] e4m3 */
+  const float* scales;       /* [B, ceil(T_max/scale_block)] */
+  const int* lens;           /* [B] on the device, or NULL: L for every sequence */
+  const void* w_ukv;         /* [d_c, n_kv*(d_nope+d_v)] */
+  void* c_hat_out;           /* [B, L, d_c] */
+  void* k_rope_out;          /* [B, L, d_rope] */
+  void* kv_out;              /* [B, L, n_kv, d_nope+d_v] */
+} gdla_qcache_read_args;
+
+gdla_status gdla_qcache_read(const gdla_qcache_read_args* args, void* stream);
+gdla_status gdla_qcache_expand(const gdla_qcache_read_args* args, void* stream);
+
+/* gdla_decode over the 8-bit cache: one new token per sequence, whose own row is
+ * already written. Same layouts, masks, head ordering and supported shapes as
+ * gdla_decode (bf16 with d_c = 512 and d_rope = 64 on the tensor cores in e4m3, with
+ * any head count; other shapes and fp32 on the CUDA cores with at most 64 query
+ * heads), and the same workspace rules.
+ * A sequence of length 0 (an empty slot of a padded batch) returns zeros. A length
+ * outside [0, T_max] is clamped into it and reported as GDLA_ERR_INVALID_ARG in the
+ * status word. */
+typedef struct {
+  int B, T_max, d_c, d_rope, n_kv, d_nope, d_v, n_noise, g, scale_block;
+  gdla_mask mask;
+  int window;
+  float softmax_scale;       /* <= 0 selects 1/sqrt(d_nope + d_rope) */
+  gdla_dtype dtype;          /* element type of q, w_ukv, gate_logits and out */
+  int rope_max_pos;          /* must be >= T_max */
+  const int* seqlens;        /* [B] int32 on the device, 0 <= seqlens[b] <= T_max */
+  const void* c_cache;       /* [B, T_max, d_c] e4m3 */
+  const void* kr_cache;      /* [B, T_max, d_rope] e4m3 */
+  const float* scales;       /* [B, ceil(T_max/scale_block)] */
+  const void* q;             /* [B, n_signal+n_noise, d_nope+d_rope], rotary part pre-RoPE */
+  const void* w_ukv;         /* [d_c, n_kv*(d_nope+d_v)] */
+  const float* rope_cos;     /* [rope_max_pos, d_rope/2] */
+  const float* rope_sin;
+  const float* lam_logits;   /* [B, n_signal] fp32 */
+  const void* gate_logits;   /* [B, n_signal, d_v] */
+  void* out;                 /* [B, n_signal, d_v] */
+  void* workspace;           /* >= gdla_qcache_decode_workspace_size(args) bytes, 256-byte aligned */
+  size_t workspace_bytes;
+} gdla_qcache_decode_args;
+
+size_t gdla_qcache_decode_workspace_size(const gdla_qcache_decode_args* args);
+gdla_status gdla_qcache_decode(const gdla_qcache_decode_args* args, void* stream);
+
 /* --------------------------------------------------------------- RoPE tables
  * The cos/sin tables every entry point takes (rope_cos, rope_sin), built on the
  * host in double precision and rounded to fp32: model set-up, like loading the
