@@ -798,13 +798,13 @@ static DecodeLayout qdecode_layout(const gdla_qcache_decode_args* a) {
   l.n_hg = (H_q + kQdecHeads - 1) / kQdecHeads;
   l.hpc = (H_q + l.n_hg - 1) / l.n_hg;
   l.n_hg = (H_q + l.hpc - 1) / l.hpc;  // (thousands of heads: no group is left empty)
-  l.part_heads = kQdecHeads;
+  l.part_heads = (l.hpc + 15) / 16 * 16;
   const long tiles_max = (long)a->B * (((long)a->T_max + kQdecTile - 1) / kQdecTile);
   l.n_ranges = (int)std::min((long)std::max(1, kQdecSMs / l.n_hg), tiles_max);
   const size_t records = ((size_t)l.n_ranges + a->B) * l.n_hg;
   size_t off = kStatusBytes;
   l.qimg = off;
-  off = align256(off + (size_t)a->B * l.n_hg * kQdecImageBytes);
+  off = align256(off + (size_t)a->B * l.n_hg * qdec_image_bytes(l.part_heads));
   l.seqinfo = off;
   off = align256(off + sizeof(int2) * (size_t)a->B);
   l.part_o = off;

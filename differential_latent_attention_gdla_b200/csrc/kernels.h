@@ -139,14 +139,15 @@ cudaError_t launch_qcache_read(const QcacheReadParams& p, gdla_dtype dt, cudaStr
 
 // ---- decode over the 8-bit cache. `d` as for the bf16 cache (c_cache and kr_cache are the
 // e4m3 rows); on the tensor-core path the head groups, ranges, records and images are this
-// path's own: at most kQdecHeads heads a group, kQdecTile tokens a tile, images of
-// kQdecImageBytes (hi and lo e4m3 rows of each head, then the heads' scales).
+// path's own: kQdecTile tokens a tile, at most kQdecHeads heads a group, and records and images
+// of that many rounded up to 16 (part_heads; an image holds the hi and lo e4m3 rows of its
+// heads, then the heads' scales).
 constexpr int kQdecHeads = 48;
 constexpr int kQdecTile = 128;
 constexpr int kQdecPrefetch = 2;  // tiles prefetched into L2 ahead of the ring
 constexpr int kQdecSMs = 148;     // B200
-constexpr int kQdecImageData = 2 * kQdecHeads * 576;
-constexpr int kQdecImageBytes = (kQdecImageData + 4 * kQdecHeads + 255) / 256 * 256;
+__host__ __device__ constexpr int qdec_image_data(int heads) { return 2 * heads * 576; }
+__host__ __device__ constexpr int qdec_image_bytes(int heads) { return (qdec_image_data(heads) + 4 * heads + 255) / 256 * 256; }
 struct QdecodeParams {
   DecodeParams d;
   const float* scales;

@@ -3,28 +3,32 @@
 // tokens), and both products of the attention run on it as it is stored:
 //   S_hj = s_j (q~_h . row8_j)            q~ = tau log2e [W_UK q_nope | RoPE(q_rope)]
 //   O_h  = sum_j 2^(S_hj) s_j c8_j        (over the sum of 2^(S_hj))
-//   S^T[tokens x heads] = row8[tokens x 576] . q8^T                (M = 128, N = 96)
-//   O^T[512 x heads]   += c8^T[512 x tokens] . w8^T[tokens x heads]  (M = 4 x 128, N = 48)
+//   S^T[tokens x 2 heads] = row8[tokens x 576] . q8^T                  (M = 128, N = 96)
+//   O^T[512 x 2 heads]   += c8^T[512 x tokens] . w8^T[tokens x 2 heads]  (M = 4 x 128, N = 96)
 // The tensor cores take 8-bit operands on both sides, so the other operand of each product
-// is split into two 8-bit terms, which cost no precision against a bf16 operand:
-//   * q~ / 2^k = hi + lo / 16, both e4m3 (4 + 4 significant bits and the sign of the
-//     remainder; relative rounding 6e-4 rms, bf16's is 1.6e-3): 48 heads take 96 columns
-//     of one MMA, and the softmax adds the two halves;
-//   * w = 2^(S - M) s_j = hi + lo, hi in e4m3 and lo in e5m2, whose larger exponent range
-//     holds the remainder without a scale of its own: two MMAs into one accumulator. With
-//     w <= 430 the smallest remainder kept is 2^-17, 2^-23 of the largest weight.
+// is split into two e4m3 terms, x = hi + lo / 16 (4 + 4 significant bits and the sign of the
+// remainder: relative rounding at most 2^-8, 6e-4 rms; bf16's is 1.6e-3 rms). Both terms are
+// columns of one MMA, which so reads the cached tile from shared memory once (the rate of an
+// 8-bit MMA of this width is that of its shared-memory reads), and the two halves are added
+// when the accumulator is read:
+//   * q~ / 2^k, 2^k chosen for each head: its largest element fills the e4m3 range;
+//   * w = 2^(S + log2 s_j - M + 6) <= 2^8.75 < 448. The smallest step kept is 2^-13, 2^-19 of
+//     the largest weight (2^-22 when M lags): next to the rounding of the other weights, which
+//     is relative, this matters only for weights that add up to nothing.
 // A scale enters twice, both times outside the products: it multiplies the score, and it
-// is part of the weight (the reference M is the running maximum of S + log2 s).
+// is part of the weight (the reference M is the running maximum of S + log2 s). The sum of
+// 2^S is kept in fp32 from the weights before their rounding.
 //
 // Split: the visible 128-token tiles of all sequences are numbered in sequence order, and
 // CTA r of a head group takes tiles [r W / R, (r + 1) W / R): equal shares, no tail wave.
 // A share writes one partial (M, l, O) per sequence it touches, to record r + b; the
 // combine kernel merges the records of a sequence.
 //
-// Block: 384 threads. Warp 0 loads tiles (TMA, two stages of 72 KB, L2 prefetch ahead);
-// warp 1 issues the score MMAs, warp 2 the value MMAs, warp 3 loads query images; warps
-// 4-11 are the softmax: a thread owns one token (TMEM lane) and 24 heads. Every wait is
-// bounded and reports GDLA_ERR_TIMEOUT.
+// Block: warp 0 loads tiles (TMA, two stages of 72 KB released in halves, L2 prefetch ahead);
+// warp 1 issues the score MMAs, warp 2 the value MMAs, warp 3 loads query images; the others
+// are the softmax, a group of four warps for each 16 of the up to 48 heads: a thread owns
+// one token (TMEM lane) and 16 heads, and the four warps of a group agree on their heads'
+// references by a barrier of their own. Every wait is bounded and reports GDLA_ERR_TIMEOUT.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -36,57 +40,55 @@ namespace gdla {
 namespace q8 {
 
 constexpr int DC = 512, DR = 64;
-constexpr int TT = kQdecTile;                    // cache tokens per tile (M of the score MMA)
-constexpr int NH = kQdecHeads;                   // query heads per CTA
-constexpr int NQ = 2 * NH;                       // hi and lo rows of the query operand
-constexpr int HT = NH / 2;                       // heads per softmax thread
-constexpr int BOX = TT * 128, RBOX = TT * 64;    // a 128-column box of the tile; the rotary box
+constexpr int TT = kQdecTile;                  // cache tokens per tile (M of the score MMA)
+constexpr int HALF = TT / 2;                   // tokens of a stage half
+constexpr int HT = 16;                         // heads per softmax thread
+constexpr int BOX = TT * 128, RBOX = TT * 64;  // a 128-column box of the tile; the rotary box
 constexpr int TILE = 4 * BOX + RBOX;
-constexpr int QBOX = NQ * 128, QRBOX = NQ * 64;  // the same of the query image
-constexpr int QIMG = 4 * QBOX + QRBOX;           // followed in memory by the NH head scales
 constexpr int STAGES = 2;
-constexpr int PPART = TT * 64;                   // weights: TT tokens x 64 heads, one byte (hi; then lo)
-constexpr int OFF_TILES = QIMG;
-constexpr int OFF_P = OFF_TILES + STAGES * TILE;
-constexpr int OFF_SH = OFF_P + 2 * PPART;
-constexpr int NSW = 8;                           // softmax warps
-constexpr int NT = 32 * (4 + NSW);
-constexpr uint32_t COL_S = 0;                    // S^T of tile k at COL_S + NQ (k & 1)
-constexpr uint32_t COL_O = 2 * NQ;               // O^T M-tile mt at COL_O + NH mt
-constexpr float kBase = 6.f;                     // weights are 2^(S + log2 s - M + kBase)
-constexpr float kThr = 2.75f;                    // M moves when exceeded by this: w <= 2^8.75 < 448
-constexpr float kMinScale = 8.6736174e-19f;      // 2^-60: keeps 1/s finite whatever the scales hold
-static_assert(QIMG == kQdecImageData && QIMG % 1024 == 0 && TILE % 1024 == 0, "1024-byte swizzle atoms");
-static_assert(NQ % 16 == 0 && NH % 16 == 0 && HT == 24, "MMA N; 24 = a 16- and an 8-column TMEM load");
-static_assert(COL_O + 4 * NH <= 512, "TMEM columns");
+constexpr int PBYTES = TT * 128;               // weights: TT tokens x (hi, lo) heads, one byte each
+constexpr uint32_t COL_S = 0;                  // S^T; then O^T of M-tile mt at NQ (1 + mt)
+constexpr float kBase = 6.f;                   // weights are 2^(S + log2 s - M + kBase)
+constexpr float kThr = 2.75f;                  // M moves when exceeded by this: w <= 2^8.75 < 448
+constexpr float kMinScale = 8.6736174e-19f;    // 2^-60: keeps 1/s finite whatever the scales hold
 
-struct Shared {
-  uint64_t full[STAGES], empty[STAGES];
-  uint64_t s_full[2], s_free[2], p_full, p_free;
-  uint64_t q_full, q_free, seg_done, mma_done;
-  uint32_t tmem_slot;
-  int abort_flag;
-  int b0;
-  int R;
-  long long p0, start, end, W;
-  long long red[NT / 32];
-  float2 tab[NH];  // per head: scale of the query, M - kBase
-  float wmax[4][NH];
-  float alpha[NH];
+// the layout for head groups of 16 HG heads
+template <int HG>
+struct Lay {
+  static constexpr int NH = HT * HG, NQ = 2 * NH;          // heads; hi and lo rows of the query operand
+  static constexpr int QBOX = NQ * 128, QIMG = NQ * 576;   // 128-column box of the query image; the image
+  static constexpr int OFF_TILES = QIMG, OFF_P = OFF_TILES + STAGES * TILE, OFF_SH = OFF_P + PBYTES;
+  static constexpr int NSW = 4 * HG, NT = 32 * (4 + NSW);  // softmax warps; threads
+  struct Shared {
+    uint64_t full[STAGES], empty[2 * STAGES];
+    uint64_t s_full, s_free, p_full, p_free;
+    uint64_t q_full, q_free, seg_done, mma_done;
+    uint32_t tmem_slot;
+    int abort_flag;
+    int b0;
+    int R;
+    long long p0, start, end, W;
+    long long red[NT / 32];
+    float4 hx[NH / 4], hm[NH / 4];  // per head: scale of the query; kBase - M
+    float wmax[4][NH];
+    float alpha[NH];
+  };
+  static constexpr int SMEM = OFF_SH + (int)sizeof(Shared);
+  static_assert(QIMG % 1024 == 0 && TILE % 1024 == 0, "1024-byte swizzle atoms");
+  static_assert(NQ * 5 <= 512, "TMEM columns");
+  static_assert(SMEM <= 232448, "shared memory of one CTA");
 };
-constexpr int SMEM = OFF_SH + (int)sizeof(Shared);
-static_assert(SMEM <= 232448, "shared memory of one CTA");
 
 struct Args {
-  int B, T_max, sliding, window, H_q, n_hg, hpc, n_ranges, sl, n_blocks;
+  int B, T_max, sliding, window, H_q, n_hg, hpc, n_ranges, sl, n_blocks, img_bytes;
   const int* seqlens;
   const uint8_t* c8;
   const uint8_t* kr8;
   const float* scales;
   const uint8_t* qimg;
   int2* seqinfo;
-  float* part_o;   // [records][NH][512]
-  float* part_ml;  // [records][NH][2]
+  float* part_o;   // [records][heads of a group][512]
+  float* part_ml;  // [records][heads of a group][2]
   int* status;
 };
 
@@ -99,7 +101,7 @@ __device__ __forceinline__ SeqTiles seq_tiles(const Args& a, int b) {
   s.Tb = min(max(__ldg(a.seqlens + b), 0), a.T_max);
   s.lo = a.sliding ? max(0, s.Tb - a.window) : 0;
   s.jt0 = s.lo / TT;
-  s.n = (s.Tb + TT - 1) / TT - s.jt0;
+  s.n = (int)(((long long)s.Tb + TT - 1) / TT) - s.jt0;
   return s;
 }
 struct Walker {
@@ -130,38 +132,44 @@ __device__ __forceinline__ int range_of(long long t, long long W, int R) {
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
+__device__ __forceinline__ uint32_t e4m3x2(__half2 h) {
+  return __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&h), __NV_SATFINITE, __NV_E4M3);
+}
 __device__ __forceinline__ __half2 e4m3x2_to_half2(uint32_t two) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
   return *reinterpret_cast<const __half2*>(&h);
 }
-// two weights as hi (e4m3) and lo (e5m2) pairs. The remainder is formed in fp16, whose 11 bits
-// hold the 4 of hi and more than the 3 of lo
+// two weights as pairs of hi and 16 lo. The remainder is formed in fp16, whose 11 bits hold
+// the 4 of hi and more than the 4 of lo
 __device__ __forceinline__ void split_weights(float w0, float w1, uint32_t& hi, uint32_t& lo) {
   const __half2 w = __floats2half2_rn(w0, w1);
-  hi = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&w), __NV_SATFINITE, __NV_E4M3);
-  const __half2 r = __hsub2(w, e4m3x2_to_half2(hi));
-  lo = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&r), __NV_SATFINITE, __NV_E5M2);
+  hi = e4m3x2(w);
+  lo = e4m3x2(__hmul2(__hsub2(w, e4m3x2_to_half2(hi)), __float2half2_rn(16.f)));
 }
-__device__ __forceinline__ bool bar_or(bool pred) { return sm100::named_bar_or(1, 32 * NSW, pred); }
-__device__ __forceinline__ void bar_sync() { sm100::named_bar_sync(1, 32 * NSW); }
-// 24 consecutive TMEM columns
-__device__ __forceinline__ void tmem_ld24(uint32_t t, uint32_t (&r)[HT]) {
-  sm100::tmem_ld16(t, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
-  sm100::tmem_ld8(t + 16, *reinterpret_cast<uint32_t(*)[8]>(&r[16]));
+__device__ __forceinline__ float2 f2(const uint32_t (&r)[HT], int i) {
+  return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+}
+// pair i of 16 per-head values
+__device__ __forceinline__ float2 pair(const float4* v, int i) {
+  const float4 x = v[i >> 1];
+  return i & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
 }
 
 }  // namespace q8
 
-__global__ void __launch_bounds__(q8::NT, 1)
+template <int HG>
+__global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
     qdecode_split_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmR,
                          const q8::Args a) {
   using namespace sm100;
   using namespace q8;
+  using L = Lay<HG>;
+  constexpr int NH = L::NH, NQ = L::NQ, NT = L::NT, NSW = L::NSW;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* qs = smem;                  // query image: 4 boxes of [96 x 128 B], one of [96 x 64 B]
-  uint8_t* tiles = smem + OFF_TILES;   // stages: 4 boxes of [128 tokens x 128 B], one of [128 x 64 B]
-  uint8_t* ps = smem + OFF_P;          // weights [128 tokens x 64 B]: hi, lo
-  Shared& sh = *reinterpret_cast<Shared*>(smem + OFF_SH);
+  uint8_t* qs = smem;                     // query image: 4 boxes of [NQ x 128 B], one of [NQ x 64 B]
+  uint8_t* tiles = smem + L::OFF_TILES;   // stages: 4 boxes of [128 tokens x 128 B], one of [128 x 64 B]
+  uint8_t* ps = smem + L::OFF_P;          // weights [128 tokens x 128 B]: NH hi, NH lo
+  typename L::Shared& sh = *reinterpret_cast<typename L::Shared*>(smem + L::OFF_SH);
   volatile int& abort_flag = sh.abort_flag;
 
   grid_dep_launch();
@@ -242,14 +250,10 @@ __global__ void __launch_bounds__(q8::NT, 1)
   const int nh = min(a.hpc, a.H_q - hg * a.hpc);  // query heads of this head group
 
   if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(smem_u32(&sh.full[i]), 1);
-      mbar_init(smem_u32(&sh.empty[i]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.s_free[i]), NSW);
-    }
+    for (int i = 0; i < STAGES; ++i) mbar_init(smem_u32(&sh.full[i]), 1);
+    for (int i = 0; i < 2 * STAGES; ++i) mbar_init(smem_u32(&sh.empty[i]), 1);
+    mbar_init(smem_u32(&sh.s_full), 1);
+    mbar_init(smem_u32(&sh.s_free), NSW);
     mbar_init(smem_u32(&sh.p_full), NSW);
     mbar_init(smem_u32(&sh.p_free), 1);
     mbar_init(smem_u32(&sh.q_full), 1);
@@ -287,13 +291,7 @@ __global__ void __launch_bounds__(q8::NT, 1)
       int k = 0;
       for (; k < n_tiles && !abort_flag; ++k) {
         const int st = k % STAGES;
-        if (k >= STAGES) {
-          if (k + kQdecPrefetch < n_tiles) prefetch(start + k + kQdecPrefetch);
-          if (!mbar_wait(smem_u32(&sh.empty[st]), ((k / STAGES) & 1) ^ 1, a.status, 501, &abort_flag)) {
-            abort_flag = 1;
-            break;
-          }
-        }
+        if (k >= STAGES && k + kQdecPrefetch < n_tiles) prefetch(start + k + kQdecPrefetch);
         const long long t = start + k;
         wl.seek(t);
         if (t == wl.pb && hg == 0)  // this CTA holds the sequence's first tile: record who covers it
@@ -301,9 +299,21 @@ __global__ void __launch_bounds__(q8::NT, 1)
         const int j0 = wl.token0(t);
         const uint32_t bar = smem_u32(&sh.full[st]);
         const uint32_t dst = smem_u32(tiles + st * TILE);
-        mbar_expect_tx(bar, TILE);
-        for (int bx = 0; bx < 4; ++bx) tma_load_3d(dst + bx * BOX, &tmC, bar, bx * 128, j0, wl.b);
-        tma_load_3d(dst + 4 * BOX, &tmR, bar, 0, j0, wl.b);
+        bool ok = true;
+        for (int hf = 0; hf < 2 && ok; ++hf) {
+          if (k >= STAGES)
+            ok = mbar_wait(smem_u32(&sh.empty[2 * st + hf]), ((k / STAGES) & 1) ^ 1, a.status, 501, &abort_flag);
+          if (!ok) break;
+          if (hf == 0) mbar_expect_tx(bar, TILE);
+          for (int bx = 0; bx < 4; ++bx)
+            tma_load_3d(dst + bx * BOX + hf * (BOX / 2), &tmC, bar, bx * 128, j0 + HALF * hf, wl.b);
+          tma_load_3d(dst + 4 * BOX + hf * (RBOX / 2), &tmR, bar, 0, j0 + HALF * hf, wl.b);
+        }
+        if (!ok) {
+          abort_flag = 1;
+          ++k;  // (the tile's first half may be on its way)
+          break;
+        }
       }
       if (abort_flag)
         for (int q = (k > STAGES ? k - STAGES : 0); q < k; ++q)
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(q8::NT, 1)
     if (lane == 0) {
       constexpr uint32_t id = idesc_f8_f32(TT, NQ, kF8E4m3, kF8E4m3, false, false);
       const uint64_t q128 = sdesc_sw128(smem_u32(qs), 16, 1024);
-      const uint64_t q64 = sdesc_sw64(smem_u32(qs + 4 * QBOX), 16, 512);
+      const uint64_t q64 = sdesc_sw64(smem_u32(qs + 4 * L::QBOX), 16, 512);
       Walker w;
       w.init(a, b0, p0);
       int seg = -1;
@@ -325,21 +335,20 @@ __global__ void __launch_bounds__(q8::NT, 1)
         const bool first = k == 0 || t == w.pb, last = k == n_tiles - 1 || t == w.pb + w.st.n - 1;
         if (first) ok = mbar_wait(smem_u32(&sh.q_full), ++seg & 1, a.status, 510, &abort_flag);
         if (ok) ok = mbar_wait(smem_u32(&sh.full[k % STAGES]), (k / STAGES) & 1, a.status, 511, &abort_flag);
-        // the softmax of tile k - 2 has loaded this S^T buffer
-        if (ok && k >= 2) ok = mbar_wait(smem_u32(&sh.s_free[k & 1]), ((k >> 1) & 1) ^ 1, a.status, 512, &abort_flag);
+        // the softmax of tile k - 1 has loaded S^T
+        if (ok && k >= 1) ok = mbar_wait(smem_u32(&sh.s_free), (k - 1) & 1, a.status, 512, &abort_flag);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tb = smem_u32(tiles + (k % STAGES) * TILE);
         const uint64_t c128 = sdesc_sw128(tb, 16, 1024), c64 = sdesc_sw64(tb + 4 * BOX, 16, 512);
-        const uint32_t d = tmem + COL_S + NQ * (k & 1);
 #pragma unroll
         for (int kk = 0; kk < 16; ++kk) {
           const uint32_t bx = kk >> 2, off = (kk & 3) * 32;
-          mma_f8_ss(d, c128 + ((bx * BOX + off) >> 4), q128 + ((bx * QBOX + off) >> 4), id, kk > 0);
+          mma_f8_ss(tmem + COL_S, c128 + ((bx * BOX + off) >> 4), q128 + ((bx * L::QBOX + off) >> 4), id, kk > 0);
         }
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk) mma_f8_ss(d, c64 + 2 * kk, q64 + 2 * kk, id, 1);
-        mma_commit(smem_u32(&sh.s_full[k & 1]));
+        for (int kk = 0; kk < 2; ++kk) mma_f8_ss(tmem + COL_S, c64 + 2 * kk, q64 + 2 * kk, id, 1);
+        mma_commit(smem_u32(&sh.s_full));
         if (last) mma_commit(smem_u32(&sh.q_free));  // the query image may be replaced
       }
       if (!ok) abort_flag = 1;
@@ -349,9 +358,8 @@ __global__ void __launch_bounds__(q8::NT, 1)
   } else if (warp == 2) {
     // ---------------------------------------------------------- value MMAs
     if (lane == 0) {
-      constexpr uint32_t id_hi = idesc_f8_f32(128, NH, kF8E4m3, kF8E4m3, true, true);
-      constexpr uint32_t id_lo = idesc_f8_f32(128, NH, kF8E4m3, kF8E5m2, true, true);
-      const uint64_t w_hi = sdesc_sw64(smem_u32(ps), 64, 512), w_lo = sdesc_sw64(smem_u32(ps + PPART), 64, 512);
+      constexpr uint32_t id = idesc_f8_f32(128, NQ, kF8E4m3, kF8E4m3, true, true);
+      const uint64_t wd = sdesc_sw128(smem_u32(ps), BOX, 1024);
       Walker w;
       w.init(a, b0, p0);
       bool ok = true;
@@ -366,15 +374,15 @@ __global__ void __launch_bounds__(q8::NT, 1)
         tc_fence_after();
         const uint64_t c = sdesc_sw128(smem_u32(tiles + (k % STAGES) * TILE), BOX, 1024);
 #pragma unroll
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int kk = 0; kk < TT / 32; ++kk) {  // 32 tokens: 4096 bytes of a box and of the weights
 #pragma unroll
-          for (int kk = 0; kk < TT / 32; ++kk) {  // 32 tokens: 4096 bytes of a box, 2048 of the weights
-            const uint64_t ca = c + ((mt * BOX + kk * 4096) >> 4);
-            mma_f8_ss(tmem + COL_O + NH * mt, ca, w_hi + ((kk * 2048) >> 4), id_hi, (!first || kk > 0) ? 1u : 0u);
-            mma_f8_ss(tmem + COL_O + NH * mt, ca, w_lo + ((kk * 2048) >> 4), id_lo, 1u);
-          }
+          for (int mt = 0; mt < 4; ++mt)
+            mma_f8_ss(tmem + NQ * (1 + mt), c + ((mt * BOX + kk * 4096) >> 4), wd + ((kk * 4096) >> 4), id,
+                      (!first || kk > 0) ? 1u : 0u);
+          // the stage's halves go back to the producer one by one
+          if (kk == TT / 64 - 1) mma_commit(smem_u32(&sh.empty[2 * (k % STAGES)]));
         }
-        mma_commit(smem_u32(&sh.empty[k % STAGES]));
+        mma_commit(smem_u32(&sh.empty[2 * (k % STAGES) + 1]));
         mma_commit(smem_u32(&sh.p_free));
         if (last) mma_commit(smem_u32(&sh.seg_done));  // O^T holds the whole sequence share
       }
@@ -395,8 +403,8 @@ __global__ void __launch_bounds__(q8::NT, 1)
         if (seg > 0) ok = mbar_wait(smem_u32(&sh.q_free), (seg - 1) & 1, a.status, 531, &abort_flag);
         if (!ok) break;
         const uint32_t bar = smem_u32(&sh.q_full);
-        mbar_expect_tx(bar, QIMG);
-        bulk_load(smem_u32(qs), a.qimg + ((long long)w.b * a.n_hg + hg) * kQdecImageBytes, QIMG, bar);
+        mbar_expect_tx(bar, L::QIMG);
+        bulk_load(smem_u32(qs), a.qimg + ((long long)w.b * a.n_hg + hg) * a.img_bytes, L::QIMG, bar);
         t = w.pb + w.st.n;  // the next sequence's first tile
       }
       if (!ok) abort_flag = 1;
@@ -404,10 +412,15 @@ __global__ void __launch_bounds__(q8::NT, 1)
     }
   } else {
     // ------------------------------------------------------------- softmax
-    const int st_id = tid - 128;            // 0 .. 255
-    const int q4 = warp & 3, hf = (warp - 4) >> 2, hb = hf * HT;
-    const int tl = q4 * 32 + lane;          // this thread's token of the tile
+    const int grp = (warp - 4) >> 2, q4 = warp & 3, hb = grp * HT;
+    const int tl = q4 * 32 + lane;  // this thread's token of the tile; its index in the group
     const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+    const uint32_t tS = tmem + lane_base + COL_S + hb;
+    float4* hx = sh.hx + hb / 4;
+    float4* hm = sh.hm + hb / 4;
+    float* hm1 = reinterpret_cast<float*>(hm);
+    auto grp_or = [&](bool pred) { return named_bar_or(1 + grp, 128, pred); };
+    auto grp_sync = [&]() { named_bar_sync(1 + grp, 128); };
     Walker w, wn;
     w.init(a, b0, p0);
     wn.init(a, b0, p0);
@@ -419,145 +432,138 @@ __global__ void __launch_bounds__(q8::NT, 1)
       return j >= wn.st.lo && j < wn.st.Tb ? __ldg(a.scales + (long long)wn.b * a.n_blocks + (j >> a.sl)) : 1.f;
     };
     float s_next = load_scale(start);
-    float lp[HT];
+    float2 lp[HT / 2];
     int seg = -1;
     bool ok = true, bad = false;
     for (int k = 0; k < n_tiles; ++k) {
       const long long t = start + k;
       w.seek(t);
       const bool first = k == 0 || t == w.pb, last = k == n_tiles - 1 || t == w.pb + w.st.n - 1;
-      const float sc = s_next;
+      const float sc = fmaxf(s_next, kMinScale);
       if (k + 1 < n_tiles) s_next = load_scale(t + 1);
-      const int j0 = w.token0(t), j = j0 + tl;
+      const int j = w.token0(t) + tl;
       const bool valid = j >= w.st.lo && j < w.st.Tb;
       if (first) {
         ++seg;
-        if (st_id < NH) {
+        if (tl < HT) {
           const float* hs = reinterpret_cast<const float*>(
-              a.qimg + ((long long)w.b * a.n_hg + hg) * kQdecImageBytes + QIMG);
-          sh.tab[st_id] = make_float2(hs[st_id], -INFINITY);
+              a.qimg + ((long long)w.b * a.n_hg + hg) * a.img_bytes + L::QIMG);
+          reinterpret_cast<float*>(hx)[tl] = hs[hb + tl];
+          hm1[tl] = INFINITY;
         }
 #pragma unroll
-        for (int h = 0; h < HT; ++h) lp[h] = 0.f;
-        bar_sync();
+        for (int i = 0; i < HT / 2; ++i) lp[i] = make_float2(0.f, 0.f);
+        grp_sync();
       }
-      const float sc1 = fmaxf(sc, kMinScale), ls = __log2f(sc1), inv_s = __frcp_rn(sc1);
-      bad |= !mbar_wait(smem_u32(&sh.s_full[k & 1]), (k >> 1) & 1, a.status, 522, &abort_flag);
+      const float ls = __log2f(sc), inv_s = __frcp_rn(sc);
+      const float2 s2 = make_float2(sc, sc), ls2 = make_float2(ls, ls), i2 = make_float2(inv_s, inv_s);
+      bad |= !mbar_wait(smem_u32(&sh.s_full), k & 1, a.status, 522, &abort_flag);
       __syncwarp();
-      float dot[HT], e[HT];
-      bool exceed = false;
+      float2 dot[HT / 2], e[HT / 2];
       {
         tc_fence_after();
         uint32_t xh[HT], xl[HT];
-        const uint32_t tS = tmem + lane_base + COL_S + NQ * (k & 1) + hb;
-        tmem_ld24(tS, xh);
-        tmem_ld24(tS + NH, xl);
+        tmem_ld16(tS, xh);
+        tmem_ld16(tS + NH, xl);
         tmem_wait_ld();
         tc_fence_before();
-        mbar_arrive_warp(smem_u32(&sh.s_free[k & 1]));
+        mbar_arrive_warp(smem_u32(&sh.s_free));
 #pragma unroll
-        for (int h = 0; h < HT; ++h) {
-          dot[h] = fmaf(__uint_as_float(xl[h]), 0.0625f, __uint_as_float(xh[h]));
-          const float2 tb = sh.tab[hb + h];
-          e[h] = valid ? fmaf(dot[h], tb.x * sc, ls - tb.y) : -INFINITY;
-          exceed |= e[h] > kBase + kThr;
-        }
+        for (int i = 0; i < HT / 2; ++i) dot[i] = ffma2(f2(xl, i), make_float2(0.0625f, 0.0625f), f2(xh, i));
       }
-      if (bar_or(exceed || bad)) {
-        if (bar_or(bad)) {
+#pragma unroll
+      for (int i = 0; i < HT / 2; ++i) e[i] = ffma2(dot[i], fmul2(pair(hx, i), s2), fadd2(pair(hm, i), ls2));
+      if (!valid) {  // (whatever the row held)
+#pragma unroll
+        for (int i = 0; i < HT / 2; ++i) e[i] = make_float2(-INFINITY, -INFINITY);
+      }
+      float mx = fmaxf(e[0].x, e[0].y);
+#pragma unroll
+      for (int i = 1; i < HT / 2; ++i) mx = fmax3(mx, e[i].x, e[i].y);
+      if (grp_or(mx > kBase + kThr || bad)) {
+        if (grp_or(bad)) {
           ok = false;
           break;
         }
         // some head's reference moves: the tile's maximum of S + log2 s per head
 #pragma unroll
-        for (int h = 0; h < HT; ++h) {
-          float v = valid ? fmaf(dot[h], sh.tab[hb + h].x * sc, ls) : -INFINITY;
+        for (int i = 0; i < HT / 2; ++i) {
+          float2 v = ffma2(dot[i], fmul2(pair(hx, i), s2), ls2);
+          if (!valid) v = make_float2(-INFINITY, -INFINITY);
 #pragma unroll
-          for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-          if (lane == 0) sh.wmax[q4][hb + h] = v;
+          for (int o = 16; o; o >>= 1) {
+            v.x = fmaxf(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
+            v.y = fmaxf(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
+          }
+          if (lane == 0) {
+            sh.wmax[q4][hb + 2 * i] = v.x;
+            sh.wmax[q4][hb + 2 * i + 1] = v.y;
+          }
         }
-        bar_sync();
+        grp_sync();
         bool resc = false;
-        if (st_id < NH) {
-          const float tm = fmaxf(fmaxf(sh.wmax[0][st_id], sh.wmax[1][st_id]), fmaxf(sh.wmax[2][st_id], sh.wmax[3][st_id]));
-          const float m_old = sh.tab[st_id].y + kBase;
+        if (tl < HT) {
+          const int h = hb + tl;
+          const float tm = fmaxf(fmaxf(sh.wmax[0][h], sh.wmax[1][h]), fmaxf(sh.wmax[2][h], sh.wmax[3][h]));
+          const float m_old = kBase - hm1[tl];
           const bool up = tm > m_old + kThr;  // (also when m_old is -inf and tm is not)
           resc = up && m_old > -INFINITY;
-          sh.alpha[st_id] = ex2_approx(up ? m_old - tm : 0.f);  // (0 from -inf)
-          if (up) sh.tab[st_id].y = tm - kBase;
+          sh.alpha[h] = ex2_approx(up ? m_old - tm : 0.f);  // (0 from -inf)
+          if (up) hm1[tl] = kBase - tm;
         }
-        const bool any = bar_or(resc);  // (also publishes tab and alpha)
+        const bool any = grp_or(resc);  // (also publishes hm and alpha)
 #pragma unroll
-        for (int h = 0; h < HT; ++h) {
-          const float2 tb = sh.tab[hb + h];
-          lp[h] *= sh.alpha[hb + h];
-          e[h] = valid ? fmaf(dot[h], tb.x * sc, ls - tb.y) : -INFINITY;
+        for (int i = 0; i < HT / 2; ++i) {
+          lp[i] = fmul2(lp[i], make_float2(sh.alpha[hb + 2 * i], sh.alpha[hb + 2 * i + 1]));
+          e[i] = ffma2(dot[i], fmul2(pair(hx, i), s2), fadd2(pair(hm, i), ls2));
+          if (!valid) e[i] = make_float2(-INFINITY, -INFINITY);
         }
         if (any) {
           // O^T holds the tiles before k once the value MMAs of tile k - 1 have landed
-          const bool r_ok = mbar_wait(smem_u32(&sh.p_free), (k - 1) & 1, a.status, 523, &abort_flag);
-          bad |= !r_ok;
+          bad |= !mbar_wait(smem_u32(&sh.p_free), (k - 1) & 1, a.status, 523, &abort_flag);
           __syncwarp();
           tc_fence_after();
 #pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt) {
+          for (int c = 0; c < 8; ++c) {  // M-tile c / 2, hi or lo columns
             uint32_t o[HT];
-            const uint32_t ta = tmem + lane_base + COL_O + NH * mt + hb;
-            tmem_ld24(ta, o);
+            const uint32_t ta = tmem + lane_base + NQ * (1 + (c >> 1)) + NH * (c & 1) + hb;
+            tmem_ld16(ta, o);
             tmem_wait_ld();
 #pragma unroll
             for (int h = 0; h < HT; ++h) o[h] = __float_as_uint(__uint_as_float(o[h]) * sh.alpha[hb + h]);
-            tmem_st16(ta, *reinterpret_cast<uint32_t(*)[16]>(&o[0]));
-            tmem_st8(ta + 16, *reinterpret_cast<uint32_t(*)[8]>(&o[16]));
+            tmem_st16(ta, o);
           }
           tmem_wait_st();
         }
       }
-      // weights of this token: hi and lo bytes of 24 heads
+      // weights of this token: hi and lo bytes of 16 heads
       uint32_t wh[HT / 4], wl[HT / 4];
 #pragma unroll
       for (int q = 0; q < HT / 4; ++q) {
-        float p[4];
+        uint32_t h[2], l[2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          p[u] = ex2_approx(e[4 * q + u]);
-          lp[4 * q + u] = fmaf(p[u], inv_s, lp[4 * q + u]);
+        for (int u = 0; u < 2; ++u) {
+          const float2 p = make_float2(ex2_approx(e[2 * q + u].x), ex2_approx(e[2 * q + u].y));
+          lp[2 * q + u] = ffma2(p, i2, lp[2 * q + u]);
+          split_weights(p.x, p.y, h[u], l[u]);
         }
-        uint32_t h0, l0, h1, l1;
-        split_weights(p[0], p[1], h0, l0);
-        split_weights(p[2], p[3], h1, l1);
-        wh[q] = h0 | (h1 << 16);
-        wl[q] = l0 | (l1 << 16);
+        wh[q] = h[0] | (h[1] << 16);
+        wl[q] = l[0] | (l[1] << 16);
       }
       // a row that is not visible may hold anything: its weight is zero, but 0 x NaN is NaN
       if (!valid) {
-        uint8_t* tb = tiles + (k % STAGES) * TILE + 2 * hf * BOX + tl * 128;
+        uint8_t* tb = tiles + (k % STAGES) * TILE + tl * 128;
+        for (int bx = grp; bx < 4; bx += HG)
 #pragma unroll
-        for (int c = 0; c < 16; ++c)
-          *reinterpret_cast<uint4*>(tb + (c >> 3) * BOX + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+          for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(tb + bx * BOX + c * 16) = make_uint4(0, 0, 0, 0);
       }
       // the weights of tile k - 1 have been consumed
       if (k >= 1) bad |= !mbar_wait(smem_u32(&sh.p_free), (k - 1) & 1, a.status, 524, &abort_flag);
       __syncwarp();
-      {
-        // token row of 64 bytes, 16-byte chunks (16 heads) swizzled by bits 1..2 of the token:
-        // heads 0..23 are chunk 0 and the first half of chunk 1, heads 24..47 the rest
-        const int sw = (tl >> 1) & 3;
-        uint8_t* row = ps + tl * 64;
-        uint8_t* full_c = row + (((hf ? 2 : 0) ^ sw) << 4);
-        uint8_t* half_c = row + ((1 ^ sw) << 4) + 8 * hf;
-        if (hf) {
-          *reinterpret_cast<uint2*>(half_c) = make_uint2(wh[0], wh[1]);
-          *reinterpret_cast<uint4*>(full_c) = make_uint4(wh[2], wh[3], wh[4], wh[5]);
-          *reinterpret_cast<uint2*>(half_c + PPART) = make_uint2(wl[0], wl[1]);
-          *reinterpret_cast<uint4*>(full_c + PPART) = make_uint4(wl[2], wl[3], wl[4], wl[5]);
-        } else {
-          *reinterpret_cast<uint4*>(full_c) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
-          *reinterpret_cast<uint2*>(half_c) = make_uint2(wh[4], wh[5]);
-          *reinterpret_cast<uint4*>(full_c + PPART) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
-          *reinterpret_cast<uint2*>(half_c + PPART) = make_uint2(wl[4], wl[5]);
-        }
-      }
+      // token row of 128 bytes, 16-byte chunks (16 heads: hi of the groups, then lo) swizzled
+      // by the token's low bits
+      *reinterpret_cast<uint4*>(ps + tl * 128 + ((grp ^ (tl & 7)) << 4)) = make_uint4(wh[0], wh[1], wh[2], wh[3]);
+      *reinterpret_cast<uint4*>(ps + tl * 128 + (((HG + grp) ^ (tl & 7)) << 4)) = make_uint4(wl[0], wl[1], wl[2], wl[3]);
       fence_proxy_async_smem();
       tc_fence_before();
       mbar_arrive_warp(smem_u32(&sh.p_full));
@@ -565,37 +571,45 @@ __global__ void __launch_bounds__(q8::NT, 1)
       if (last) {
         // ---- partial of this sequence share: (M, l) per head and O^T
         const bool d_ok = mbar_wait(smem_u32(&sh.seg_done), seg & 1, a.status, 525, &abort_flag);
-        if (bar_or(!d_ok || bad)) {
+        if (grp_or(!d_ok || bad)) {
           ok = false;
           break;
         }
         tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < HT; ++h) {
-          float v = lp[h];
+        for (int i = 0; i < HT / 2; ++i) {
+          float2 v = lp[i];
 #pragma unroll
-          for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-          if (lane == 0) sh.wmax[q4][hb + h] = v;
+          for (int o = 16; o; o >>= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, o);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+          }
+          if (lane == 0) {
+            sh.wmax[q4][hb + 2 * i] = v.x;
+            sh.wmax[q4][hb + 2 * i + 1] = v.y;
+          }
         }
-        bar_sync();
+        grp_sync();
         const long long rec = ((long long)(r + w.b) * a.n_hg + hg) * NH;
-        if (st_id < nh) {
-          a.part_ml[(rec + st_id) * 2 + 0] = sh.tab[st_id].y + kBase;
-          a.part_ml[(rec + st_id) * 2 + 1] =
-              (sh.wmax[0][st_id] + sh.wmax[1][st_id]) + (sh.wmax[2][st_id] + sh.wmax[3][st_id]);
+        if (tl < HT && hb + tl < nh) {
+          const int h = hb + tl;
+          a.part_ml[(rec + h) * 2 + 0] = kBase - hm1[tl];
+          a.part_ml[(rec + h) * 2 + 1] = (sh.wmax[0][h] + sh.wmax[1][h]) + (sh.wmax[2][h] + sh.wmax[3][h]);
         }
 #pragma unroll 1
         for (int mt = 0; mt < 4; ++mt) {
-          uint32_t o[HT];
-          tmem_ld24(tmem + lane_base + COL_O + NH * mt + hb, o);
+          uint32_t oh[HT], ol[HT];
+          const uint32_t ta = tmem + lane_base + NQ * (1 + mt) + hb;
+          tmem_ld16(ta, oh);
+          tmem_ld16(ta + NH, ol);
           tmem_wait_ld();
-          float* dst = a.part_o + (rec + hb) * DC + mt * 128 + q4 * 32 + lane;
+          float* dst = a.part_o + (rec + hb) * DC + mt * 128 + tl;
 #pragma unroll
           for (int h = 0; h < HT; ++h)
-            if (hb + h < nh) dst[h * DC] = __uint_as_float(o[h]);
+            if (hb + h < nh) dst[h * DC] = fmaf(__uint_as_float(ol[h]), 0.0625f, __uint_as_float(oh[h]));
         }
         tc_fence_before();
-        bar_sync();
+        grp_sync();
       }
     }
     if (!ok || bad) abort_flag = 1;
@@ -617,7 +631,7 @@ constexpr int AB = 128;
 constexpr int AB_OP = AB * AB * 2;  // an operand: two 64-column chunks of [128 rows x 128 B]
 constexpr int AB_SMEM = 2 * AB_OP + 64;
 struct AbsorbArgs {
-  int B, T_max, n_kv, g, H_q, n_hg, hpc;
+  int B, T_max, n_kv, g, H_q, n_hg, hpc, NH;  // NH: heads of an image (kQdecHeads at most)
   float isc;
   const __nv_bfloat16* q;
   const int* seqlens;
@@ -627,12 +641,12 @@ struct AbsorbArgs {
   int* status;
 };
 // byte of dimension d of image row (hi: head; lo: NH + head)
-__device__ __forceinline__ int image_offset(int row, int d) {
-  return d < DC ? (d >> 7) * QBOX + row * 128 + ((((d & 127) >> 4) ^ (row & 7)) << 4) + (d & 15)
-                : 4 * QBOX + row * 64 + ((((d - DC) >> 4) ^ ((row >> 1) & 3)) << 4) + (d & 15);
+__device__ __forceinline__ int image_offset(int NH, int row, int d) {
+  return d < DC ? (d >> 7) * (2 * NH * 128) + row * 128 + ((((d & 127) >> 4) ^ (row & 7)) << 4) + (d & 15)
+                : 4 * (2 * NH * 128) + row * 64 + ((((d - DC) >> 4) ^ ((row >> 1) & 3)) << 4) + (d & 15);
 }
 // 16 values (already divided by the row's scale) into the hi and lo rows
-__device__ __forceinline__ void store16(uint8_t* img, int head, int d, const float (&x)[16]) {
+__device__ __forceinline__ void store16(uint8_t* img, int NH, int head, int d, const float (&x)[16]) {
   uint32_t hi[4], lo[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -647,8 +661,8 @@ __device__ __forceinline__ void store16(uint8_t* img, int head, int d, const flo
     hi[q] = hh[0] | (hh[1] << 16);
     lo[q] = ll[0] | (ll[1] << 16);
   }
-  *reinterpret_cast<uint4*>(img + image_offset(head, d)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-  *reinterpret_cast<uint4*>(img + image_offset(NH + head, d)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+  *reinterpret_cast<uint4*>(img + image_offset(NH, head, d)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+  *reinterpret_cast<uint4*>(img + image_offset(NH, NH + head, d)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 }  // namespace q8
 
@@ -666,6 +680,7 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x, z = blockIdx.z;
   const int G1 = a.g + 1, n_S = a.g * a.n_kv, rows = a.B * G1, r0 = blockIdx.y * AB;
+  const int NH = a.NH, img_data = qdec_image_data(NH), img_bytes = qdec_image_bytes(NH);
   // (the cluster's CTAs have the same shared-memory layout: all four or none pass this)
   if (smem_u32(smem) & 1023u) {
     if (tid == 0) {
@@ -785,7 +800,7 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
   const float inv = __int_as_float((127 - ex) << 23);
   if (real && done && !earlier_failure(a.status)) {
     const int hgi = head / a.hpc, lh = head - hgi * a.hpc;
-    uint8_t* img = a.qimg + ((long long)b * a.n_hg + hgi) * kQdecImageBytes;
+    uint8_t* img = a.qimg + ((long long)b * a.n_hg + hgi) * img_bytes;
     // (an infinity would saturate: a query that is not finite gives NaN, as its scores would)
     const float bad = top < INFINITY ? 0.f : NAN;
     float x[16];
@@ -794,10 +809,10 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         x[i] = fmaf(__uint_as_float(c < 2 ? v0[16 * (c & 1) + i] : v1[16 * (c & 1) + i]), inv, bad);
-      store16(img, lh, z * AB + ch * 64 + 16 * c, x);
+      store16(img, NH, lh, z * AB + ch * 64 + 16 * c, x);
     }
     if (rot) {
-      *reinterpret_cast<float*>(img + QIMG + 4 * lh) = __int_as_float((127 + ex) << 23);
+      *reinterpret_cast<float*>(img + img_data + 4 * lh) = __int_as_float((127 + ex) << 23);
 #pragma unroll
       for (int c2 = 0; c2 < 2; ++c2) {
         float y[16];
@@ -811,8 +826,8 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
           y[e] = fmaf(hi0[e], inv, bad);
           y[8 + e] = fmaf(hi1[e], inv, bad);
         }
-        store16(img, lh, DC + 16 * c2, x);
-        store16(img, lh, DC + 32 + 16 * c2, y);
+        store16(img, NH, lh, DC + 16 * c2, x);
+        store16(img, NH, lh, DC + 32 + 16 * c2, y);
       }
     }
   }
@@ -823,11 +838,11 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
     for (int bb = b_lo; bb < b_hi; ++bb)
       for (int hg2 = 0; hg2 < a.n_hg; ++hg2) {
         const int nhd = min(a.hpc, a.H_q - hg2 * a.hpc);
-        uint8_t* im = a.qimg + ((long long)bb * a.n_hg + hg2) * kQdecImageBytes;
+        uint8_t* im = a.qimg + ((long long)bb * a.n_hg + hg2) * img_bytes;
         for (int e = tid; e < (NH - nhd) * 72; e += 256) {
           const int lh = nhd + e / 72, c = e % 72, part = c / 36, d = (c % 36) * 16;
-          *reinterpret_cast<uint4*>(im + image_offset(part * NH + lh, d)) = make_uint4(0, 0, 0, 0);
-          if (c == 0) *reinterpret_cast<float*>(im + QIMG + 4 * lh) = 1.f;
+          *reinterpret_cast<uint4*>(im + image_offset(NH, part * NH + lh, d)) = make_uint4(0, 0, 0, 0);
+          if (c == 0) *reinterpret_cast<float*>(im + img_data + 4 * lh) = 1.f;
         }
       }
   }
@@ -853,7 +868,7 @@ constexpr int CB_B = DC * CB_N * 2;      // 2 MN blocks of [512 K rows x 128 B]
 constexpr int CB_SMEM = CB_A + CB_B + 64;
 constexpr int CB_T = 512;
 struct CombineArgs {
-  int B, T_max, n_kv, g, H_q, n_hg, hpc, n_ranges, spb;
+  int B, T_max, n_kv, g, H_q, n_hg, hpc, NH, n_ranges, spb;
   const int* seqlens;
   const int2* seqinfo;
   const float* part_o;
@@ -888,7 +903,7 @@ __global__ void __launch_bounds__(q8::CB_T, 1)
   }
   const int h = blockIdx.x, G1 = a.g + 1, n_S = a.g * a.n_kv;
   const int b0 = blockIdx.y * a.spb, nb = min(a.spb, a.B - b0), R = nb * G1;
-  const long long rstep = (long long)a.n_hg * NH;
+  const long long rstep = (long long)a.n_hg * a.NH;
   if (tid == 0) {
     mbar_init(smem_u32(&bar[0]), 1);
     mbar_init(smem_u32(&bar[1]), 1);
@@ -916,7 +931,7 @@ __global__ void __launch_bounds__(q8::CB_T, 1)
         // early still reads inside the records); an empty sequence has none and gives zeros
         const int2 info = a.seqinfo[b];
         const int x = min(max(info.x, 0), a.n_ranges - 1), y = min(max(info.y, x), a.n_ranges - 1);
-        rec0[tid] = ((long long)(x + b) * a.n_hg + hgi) * NH + lh;
+        rec0[tid] = ((long long)(x + b) * a.n_hg + hgi) * a.NH + lh;
         n_parts[tid] = y - x + 1;
       }
     }
@@ -1093,6 +1108,7 @@ cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s) {
     if (!w_map(&tw, d, AB)) return cudaErrorInvalidValue;
     AbsorbArgs a{};
     a.B = d.B; a.T_max = d.T_max; a.n_kv = d.n_kv; a.g = d.g; a.H_q = H_q; a.n_hg = d.n_hg; a.hpc = d.hpc;
+    a.NH = d.part_heads;
     a.isc = d.scale * kLog2e;
     a.q = reinterpret_cast<const __nv_bfloat16*>(d.q); a.seqlens = d.seqlens; a.cos_tab = d.cos_tab;
     a.sin_tab = d.sin_tab; a.qimg = d.qimg; a.status = d.status;
@@ -1107,26 +1123,33 @@ cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s) {
     CUtensorMap tc, tr;
     const uint64_t cd[3] = {(uint64_t)DC, (uint64_t)d.T_max, (uint64_t)d.B};
     const uint64_t cs[2] = {(uint64_t)DC, (uint64_t)d.T_max * DC};
-    const uint32_t cb[3] = {128, (uint32_t)TT, 1};
+    const uint32_t cb[3] = {128, (uint32_t)HALF, 1};
     const uint64_t rd[3] = {(uint64_t)DR, (uint64_t)d.T_max, (uint64_t)d.B};
     const uint64_t rs[2] = {(uint64_t)DR, (uint64_t)d.T_max * DR};
-    const uint32_t rb[3] = {64, (uint32_t)TT, 1};
+    const uint32_t rb[3] = {64, (uint32_t)HALF, 1};
     if (!make_tmap_u8(&tc, d.c_cache, 3, cd, cs, cb, 128) || !make_tmap_u8(&tr, d.kr_cache, 3, rd, rs, rb, 64))
       return cudaErrorInvalidValue;
     Args a{};
     a.B = d.B; a.T_max = d.T_max; a.sliding = d.sliding; a.window = d.window; a.H_q = H_q; a.n_hg = d.n_hg;
-    a.hpc = d.hpc; a.n_ranges = d.n_ranges; a.sl = p.sl; a.n_blocks = p.n_blocks; a.seqlens = d.seqlens;
+    a.hpc = d.hpc; a.n_ranges = d.n_ranges; a.sl = p.sl; a.n_blocks = p.n_blocks;
+    a.img_bytes = qdec_image_bytes(d.part_heads); a.seqlens = d.seqlens;
     a.c8 = (const uint8_t*)d.c_cache; a.kr8 = (const uint8_t*)d.kr_cache; a.scales = p.scales; a.qimg = d.qimg;
     a.seqinfo = d.seqinfo; a.part_o = d.part_o; a.part_ml = d.part_ml; a.status = d.status;
-    cudaError_t e = launch_dependent(qdecode_split_kernel, dim3((unsigned)d.n_hg, (unsigned)d.n_ranges), NT, SMEM, s, tc,
-                                     tr, a);
+    const dim3 grid((unsigned)d.n_hg, (unsigned)d.n_ranges);
+    cudaError_t e;
+    switch (d.part_heads / HT) {
+      case 1: e = launch_dependent(qdecode_split_kernel<1>, grid, Lay<1>::NT, Lay<1>::SMEM, s, tc, tr, a); break;
+      case 2: e = launch_dependent(qdecode_split_kernel<2>, grid, Lay<2>::NT, Lay<2>::SMEM, s, tc, tr, a); break;
+      case 3: e = launch_dependent(qdecode_split_kernel<3>, grid, Lay<3>::NT, Lay<3>::SMEM, s, tc, tr, a); break;
+      default: return cudaErrorInvalidValue;
+    }
     if (e != cudaSuccess) return e;
   }
   CUtensorMap tw;
   if (!w_map(&tw, d, 256)) return cudaErrorInvalidValue;
   CombineArgs a{};
   a.B = d.B; a.T_max = d.T_max; a.n_kv = d.n_kv; a.g = d.g; a.H_q = H_q; a.n_hg = d.n_hg; a.hpc = d.hpc;
-  a.n_ranges = d.n_ranges; a.seqlens = d.seqlens; a.seqinfo = d.seqinfo; a.part_o = d.part_o; a.part_ml = d.part_ml;
+  a.NH = d.part_heads; a.n_ranges = d.n_ranges; a.seqlens = d.seqlens; a.seqinfo = d.seqinfo; a.part_o = d.part_o; a.part_ml = d.part_ml;
   a.lam = d.lam; a.gate = reinterpret_cast<const __nv_bfloat16*>(d.gate);
   a.out = reinterpret_cast<__nv_bfloat16*>(d.out); a.status = d.status;
   // sequences per block: as few as fill one wave of blocks over the SMs, at most the 32 rows
