@@ -25,8 +25,8 @@
 // combine kernel merges the records of a sequence.
 //
 // Block: warp 0 loads tiles (TMA, two stages of 72 KB released in halves, L2 prefetch ahead);
-// warp 1 issues the score MMAs, warp 2 the value MMAs, warp 3 loads query images; the others
-// are the softmax, a group of four warps for each 16 of the up to 48 heads: a thread owns
+// warp 1 issues the MMAs, warp 2 loads query images, warp 3 idles; the others are the
+// softmax, a group of four warps for each 16 of the up to 48 heads: a thread owns
 // one token (TMEM lane) and 16 heads, and the four warps of a group agree on their heads'
 // references by a barrier of their own. Every wait is bounded and reports GDLA_ERR_TIMEOUT.
 #include <cuda_fp16.h>
@@ -149,10 +149,51 @@ __device__ __forceinline__ void split_weights(float w0, float w1, uint32_t& hi, 
 __device__ __forceinline__ float2 f2(const uint32_t (&r)[HT], int i) {
   return make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
 }
+// the largest value of a warp (one that is not a number is passed over)
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
 // pair i of 16 per-head values
 __device__ __forceinline__ float2 pair(const float4* v, int i) {
   const float4 x = v[i >> 1];
   return i & 1 ? make_float2(x.z, x.w) : make_float2(x.x, x.y);
+}
+
+// The MMAs of a tile in stage ST. The stage is a constant so that every descriptor is one plus
+// a constant.
+template <int HG, int ST>
+__device__ __forceinline__ void score_mmas(uint32_t smem, uint32_t tmem) {
+  using namespace sm100;
+  using L = Lay<HG>;
+  constexpr uint32_t id = idesc_f8_f32(TT, L::NQ, kF8E4m3, kF8E4m3, false, false);
+  const uint64_t q128 = sdesc_sw128(smem, 16, 1024), q64 = sdesc_sw64(smem + 4 * L::QBOX, 16, 512);
+  const uint64_t c128 = sdesc_sw128(smem + L::OFF_TILES + ST * TILE, 16, 1024);
+  const uint64_t c64 = sdesc_sw64(smem + L::OFF_TILES + ST * TILE + 4 * BOX, 16, 512);
+#pragma unroll
+  for (int kk = 0; kk < 16; ++kk) {
+    const uint32_t bx = kk >> 2, off = (kk & 3) * 32;
+    mma_f8_ss(tmem + COL_S, c128 + ((bx * BOX + off) >> 4), q128 + ((bx * L::QBOX + off) >> 4), id, kk > 0);
+  }
+#pragma unroll
+  for (int kk = 0; kk < 2; ++kk) mma_f8_ss(tmem + COL_S, c64 + 2 * kk, q64 + 2 * kk, id, 1);
+}
+template <int HG, int ST>
+__device__ __forceinline__ void value_mmas(uint32_t smem, uint32_t tmem, uint32_t acc, uint32_t empty0) {
+  using namespace sm100;
+  using L = Lay<HG>;
+  constexpr uint32_t id = idesc_f8_f32(128, L::NQ, kF8E4m3, kF8E4m3, true, true);
+  const uint64_t c = sdesc_sw128(smem + L::OFF_TILES + ST * TILE, BOX, 1024);
+  const uint64_t wd = sdesc_sw128(smem + L::OFF_P, BOX, 1024);
+#pragma unroll
+  for (int kk = 0; kk < TT / 32; ++kk) {  // 32 tokens: 4096 bytes of a box and of the weights
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+      mma_f8_ss(tmem + L::NQ * (1 + mt), c + ((mt * BOX + kk * 4096) >> 4), wd + ((kk * 4096) >> 4), id, kk ? 1u : acc);
+    // the stage's halves go back to the producer one by one
+    if (kk == TT / 64 - 1) mma_commit(empty0);
+  }
 }
 
 }  // namespace q8
@@ -259,7 +300,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
     mbar_init(smem_u32(&sh.q_full), 1);
     mbar_init(smem_u32(&sh.q_free), 1);
     mbar_init(smem_u32(&sh.seg_done), 1);
-    mbar_init(smem_u32(&sh.mma_done), 2);
+    mbar_init(smem_u32(&sh.mma_done), 1);
     fence_mbar_init();
     abort_flag = 0;
     prefetch_tmap(&tmC);
@@ -320,77 +361,69 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
           mbar_wait(smem_u32(&sh.full[q % STAGES]), (q / STAGES) & 1, nullptr, 0);
     }
   } else if (warp == 1) {
-    // ---------------------------------------------------------- score MMAs
+    // ---------------------------------------------------------------- MMAs
+    // One thread issues both products, so that neither's MMAs are interleaved with the other's:
+    // the scores of tile k + 1 as soon as they can run, which the softmax waits for, then the
+    // values of tile k.
     if (lane == 0) {
-      constexpr uint32_t id = idesc_f8_f32(TT, NQ, kF8E4m3, kF8E4m3, false, false);
-      const uint64_t q128 = sdesc_sw128(smem_u32(qs), 16, 1024);
-      const uint64_t q64 = sdesc_sw64(smem_u32(qs + 4 * L::QBOX), 16, 512);
-      Walker w;
-      w.init(a, b0, p0);
-      int seg = -1;
+      Walker ws, wv;
+      ws.init(a, b0, p0);
+      wv.init(a, b0, p0);
+      int ks = 0, kv = 0, seg = 0;  // next tile of the scores, of the values; query images used
+      bool new_seq = true;          // tile ks starts a sequence
       bool ok = true;
-      for (int k = 0; k < n_tiles && ok; ++k) {
-        const long long t = start + k;
-        w.seek(t);
-        const bool first = k == 0 || t == w.pb, last = k == n_tiles - 1 || t == w.pb + w.st.n - 1;
-        if (first) ok = mbar_wait(smem_u32(&sh.q_full), ++seg & 1, a.status, 510, &abort_flag);
-        if (ok) ok = mbar_wait(smem_u32(&sh.full[k % STAGES]), (k / STAGES) & 1, a.status, 511, &abort_flag);
-        // the softmax of tile k - 1 has loaded S^T
-        if (ok && k >= 1) ok = mbar_wait(smem_u32(&sh.s_free), (k - 1) & 1, a.status, 512, &abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t tb = smem_u32(tiles + (k % STAGES) * TILE);
-        const uint64_t c128 = sdesc_sw128(tb, 16, 1024), c64 = sdesc_sw64(tb + 4 * BOX, 16, 512);
-#pragma unroll
-        for (int kk = 0; kk < 16; ++kk) {
-          const uint32_t bx = kk >> 2, off = (kk & 3) * 32;
-          mma_f8_ss(tmem + COL_S, c128 + ((bx * BOX + off) >> 4), q128 + ((bx * L::QBOX + off) >> 4), id, kk > 0);
+      uint64_t t0 = 0;
+      for (uint32_t idle = 0; kv < n_tiles && ok;) {
+        // the score's operands: the tile, a sequence's query image, S^T read by the softmax
+        if (ks < n_tiles && mbar_try_wait(smem_u32(&sh.full[ks % STAGES]), (ks / STAGES) & 1) &&
+            (!new_seq || mbar_try_wait(smem_u32(&sh.q_full), seg & 1)) &&
+            (ks == 0 || mbar_try_wait(smem_u32(&sh.s_free), (ks - 1) & 1))) {
+          tc_fence_after();
+          if (ks & 1)
+            score_mmas<HG, 1>(smem_u32(smem), tmem);
+          else
+            score_mmas<HG, 0>(smem_u32(smem), tmem);
+          mma_commit(smem_u32(&sh.s_full));
+          ws.seek(start + ks);
+          seg += new_seq;
+          new_seq = start + ks == ws.pb + ws.st.n - 1;
+          if (new_seq || ks == n_tiles - 1) mma_commit(smem_u32(&sh.q_free));  // the query image may be replaced
+          ++ks;
+          idle = 0;
         }
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk) mma_f8_ss(tmem + COL_S, c64 + 2 * kk, q64 + 2 * kk, id, 1);
-        mma_commit(smem_u32(&sh.s_full));
-        if (last) mma_commit(smem_u32(&sh.q_free));  // the query image may be replaced
+        // the weights of tile kv are written; their softmax has also read the previous sequence's
+        // O^T, so a new sequence may overwrite it
+        if (kv < ks && mbar_try_wait(smem_u32(&sh.p_full), kv & 1)) {
+          const long long t = start + kv;
+          wv.seek(t);
+          const uint32_t acc = kv > 0 && t != wv.pb;
+          tc_fence_after();
+          if (kv & 1)
+            value_mmas<HG, 1>(smem_u32(smem), tmem, acc, smem_u32(&sh.empty[2]));
+          else
+            value_mmas<HG, 0>(smem_u32(smem), tmem, acc, smem_u32(&sh.empty[0]));
+          mma_commit(smem_u32(&sh.empty[2 * (kv % STAGES) + 1]));
+          mma_commit(smem_u32(&sh.p_free));
+          if (kv == n_tiles - 1 || t == wv.pb + wv.st.n - 1) mma_commit(smem_u32(&sh.seg_done));  // O^T holds the share
+          ++kv;
+          idle = 0;
+        }
+        if ((++idle & 255u) == 0) {  // bounded, like mbar_wait
+          const uint64_t now = globaltimer_ns();
+          if (idle == 256) t0 = now;
+          const bool gave_up = now - t0 > kWaitLimitNs;
+          if (gave_up) {
+            atomicCAS(a.status, 0, (int)GDLA_ERR_TIMEOUT);
+            atomicCAS(a.status + 1, 0, 511);
+          }
+          ok = !gave_up && !abort_flag && !earlier_failure(a.status);
+        }
       }
       if (!ok) abort_flag = 1;
-      mma_commit(smem_u32(&sh.mma_done));  // every MMA issued here completes before TMEM is released
+      mma_commit(smem_u32(&sh.mma_done));  // every MMA issued completes before TMEM is released
       mbar_wait(smem_u32(&sh.mma_done), 0, nullptr, 514);
     }
   } else if (warp == 2) {
-    // ---------------------------------------------------------- value MMAs
-    if (lane == 0) {
-      constexpr uint32_t id = idesc_f8_f32(128, NQ, kF8E4m3, kF8E4m3, true, true);
-      const uint64_t wd = sdesc_sw128(smem_u32(ps), BOX, 1024);
-      Walker w;
-      w.init(a, b0, p0);
-      bool ok = true;
-      for (int k = 0; k < n_tiles && ok; ++k) {
-        const long long t = start + k;
-        w.seek(t);
-        const bool first = k == 0 || t == w.pb, last = k == n_tiles - 1 || t == w.pb + w.st.n - 1;
-        // the weights of tile k are written; their softmax has also read the previous
-        // sequence's O^T, so a new sequence may overwrite it
-        ok = mbar_wait(smem_u32(&sh.p_full), k & 1, a.status, 513, &abort_flag);
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t c = sdesc_sw128(smem_u32(tiles + (k % STAGES) * TILE), BOX, 1024);
-#pragma unroll
-        for (int kk = 0; kk < TT / 32; ++kk) {  // 32 tokens: 4096 bytes of a box and of the weights
-#pragma unroll
-          for (int mt = 0; mt < 4; ++mt)
-            mma_f8_ss(tmem + NQ * (1 + mt), c + ((mt * BOX + kk * 4096) >> 4), wd + ((kk * 4096) >> 4), id,
-                      (!first || kk > 0) ? 1u : 0u);
-          // the stage's halves go back to the producer one by one
-          if (kk == TT / 64 - 1) mma_commit(smem_u32(&sh.empty[2 * (k % STAGES)]));
-        }
-        mma_commit(smem_u32(&sh.empty[2 * (k % STAGES) + 1]));
-        mma_commit(smem_u32(&sh.p_free));
-        if (last) mma_commit(smem_u32(&sh.seg_done));  // O^T holds the whole sequence share
-      }
-      if (!ok) abort_flag = 1;
-      mma_commit(smem_u32(&sh.mma_done));
-      mbar_wait(smem_u32(&sh.mma_done), 0, nullptr, 515);
-    }
-  } else if (warp == 3) {
     // -------------------------------------------------------- query images
     if (lane == 0) {
       Walker w;
@@ -410,7 +443,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
       if (!ok) abort_flag = 1;
       if (seg > 0) mbar_wait(smem_u32(&sh.q_full), (seg - 1) & 1, nullptr, 0);  // no copy is in flight at exit
     }
-  } else {
+  } else if (warp >= 4) {
     // ------------------------------------------------------------- softmax
     const int grp = (warp - 4) >> 2, q4 = warp & 3, hb = grp * HT;
     const int tl = q4 * 32 + lane;  // this thread's token of the tile; its index in the group
@@ -457,6 +490,14 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
       }
       const float ls = __log2f(sc), inv_s = __frcp_rn(sc);
       const float2 s2 = make_float2(sc, sc), ls2 = make_float2(ls, ls), i2 = make_float2(inv_s, inv_s);
+      // the score's factor and offset, ready before the score
+      float2 fa[HT / 2], fb[HT / 2];
+#pragma unroll
+      for (int i = 0; i < HT / 2; ++i) {
+        fa[i] = fmul2(pair(hx, i), s2);
+        fb[i] = fadd2(pair(hm, i), ls2);
+        asm volatile("" : "+f"(fa[i].x), "+f"(fa[i].y), "+f"(fb[i].x), "+f"(fb[i].y));
+      }
       bad |= !mbar_wait(smem_u32(&sh.s_full), k & 1, a.status, 522, &abort_flag);
       __syncwarp();
       float2 dot[HT / 2], e[HT / 2];
@@ -472,7 +513,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
         for (int i = 0; i < HT / 2; ++i) dot[i] = ffma2(f2(xl, i), make_float2(0.0625f, 0.0625f), f2(xh, i));
       }
 #pragma unroll
-      for (int i = 0; i < HT / 2; ++i) e[i] = ffma2(dot[i], fmul2(pair(hx, i), s2), fadd2(pair(hm, i), ls2));
+      for (int i = 0; i < HT / 2; ++i) e[i] = ffma2(dot[i], fa[i], fb[i]);
       if (!valid) {  // (whatever the row held)
 #pragma unroll
         for (int i = 0; i < HT / 2; ++i) e[i] = make_float2(-INFINITY, -INFINITY);
@@ -485,16 +526,13 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
           ok = false;
           break;
         }
-        // some head's reference moves: the tile's maximum of S + log2 s per head
+        // some head's reference has to move: each that can goes to the tile's maximum of S + log2 s
 #pragma unroll
         for (int i = 0; i < HT / 2; ++i) {
           float2 v = ffma2(dot[i], fmul2(pair(hx, i), s2), ls2);
           if (!valid) v = make_float2(-INFINITY, -INFINITY);
-#pragma unroll
-          for (int o = 16; o; o >>= 1) {
-            v.x = fmaxf(v.x, __shfl_xor_sync(0xffffffffu, v.x, o));
-            v.y = fmaxf(v.y, __shfl_xor_sync(0xffffffffu, v.y, o));
-          }
+          v.x = warp_max(v.x);
+          v.y = warp_max(v.y);
           if (lane == 0) {
             sh.wmax[q4][hb + 2 * i] = v.x;
             sh.wmax[q4][hb + 2 * i + 1] = v.y;
@@ -506,7 +544,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
           const int h = hb + tl;
           const float tm = fmaxf(fmaxf(sh.wmax[0][h], sh.wmax[1][h]), fmaxf(sh.wmax[2][h], sh.wmax[3][h]));
           const float m_old = kBase - hm1[tl];
-          const bool up = tm > m_old + kThr;  // (also when m_old is -inf and tm is not)
+          const bool up = tm > m_old;  // (also when m_old is -inf and tm is not)
           resc = up && m_old > -INFINITY;
           sh.alpha[h] = ex2_approx(up ? m_old - tm : 0.f);  // (0 from -inf)
           if (up) hm1[tl] = kBase - tm;
