@@ -15,6 +15,7 @@ library's CUDA kernels. PyTorch supplies device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -341,9 +342,14 @@ def decode_noalloc(c_cache, kr_cache, q, w_ukv, rope_cos, rope_sin, lam_logits, 
 
 
 # ----------------------------------------------------------- 8-bit latent cache
+# (These calls are a decode step's, several a layer, so the binding's own time counts: the
+# stream comes as a raw handle where torch offers one, 0.1 us against 2 to 3, and a tensor's
+# device, layout and address are read together.)
 _Q8 = (torch.float8_e4m3fn, torch.uint8)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+@functools.lru_cache(maxsize=256)
 def qcache_scale_blocks(T_max: int, scale_block: int) -> int:
     """Scales of one sequence of a T_max-token 8-bit cache: ceil(T_max / scale_block)."""
     n = int(_lib().gdla_qcache_scale_blocks(int(T_max), int(scale_block)))
@@ -364,30 +370,48 @@ def _qcache_dims(c_cache, kr_cache, scales, scale_block):
     if c_cache.dtype not in _Q8 or kr_cache.dtype not in _Q8:
         raise ValueError("an 8-bit cache is float8_e4m3fn (or its bytes as uint8)")
     B, T_max, d_c = c_cache.shape
-    if tuple(kr_cache.shape[:2]) != (B, T_max):
+    kr_B, kr_T, d_rope = kr_cache.shape
+    if kr_B != B or kr_T != T_max:
         raise ValueError("c_cache and kr_cache must be [B, T_max, ...] of the same B and T_max")
-    if scales.dtype != torch.float32 or tuple(scales.shape) != (B, qcache_scale_blocks(T_max, scale_block)):
+    if scales.dtype != torch.float32 or scales.shape != (B, qcache_scale_blocks(T_max, scale_block)):
         raise ValueError("scales must be fp32 [B, ceil(T_max / scale_block)]")
-    return B, T_max, d_c, kr_cache.shape[2]
+    return B, T_max, d_c, d_rope
 
 
 def _same(t, name, shape, dtype=None):
-    if t is not None and (tuple(t.shape) != tuple(shape) or (dtype is not None and t.dtype != dtype)):
+    if t is not None and (t.shape != shape or (dtype is not None and t.dtype != dtype)):
         raise ValueError(f"{name} must be {list(shape)}" + (f" {dtype}" if dtype is not None else ""))
 
 
-def _call(fn, a, tensors, stream, what):
-    """The call with the tensors' device current, on ``stream`` or that device's current stream."""
-    t = tensors[0]
-    if any(x is not None and x.device != t.device for x in tensors):
-        raise ValueError("the tensors of a call must be on one device")
-    if stream is None:
-        stream = torch.cuda.current_stream(t.device)
-    if t.device.index == torch.cuda.current_device():
-        _abi.check(fn(ctypes.byref(a), _stream(stream)), what)
+def _ptrs(device: int, *tensors):
+    """Addresses of the tensors, all contiguous and on CUDA device ``device``."""
+    out = []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        if t.get_device() != device or device < 0:
+            raise ValueError("the tensors of a call must be on one device" if t.is_cuda and device >= 0 else
+                             "GDLA tensors must be CUDA device tensors")
+        if not t.is_contiguous():
+            raise ValueError("GDLA tensors must be contiguous (row-major)")
+        out.append(t.data_ptr())
+    return out
+
+
+def _call(fn, a, device: int, stream, what):
+    """The call with CUDA device ``device`` current, on ``stream`` or that device's current stream."""
+    if stream is not None:
+        stream = _stream(stream)
+    elif _raw_stream is not None:
+        stream = _raw_stream(device)
     else:
-        with torch.cuda.device(t.device):
-            _abi.check(fn(ctypes.byref(a), _stream(stream)), what)
+        stream = torch.cuda.current_stream(device).cuda_stream
+    if device == torch.cuda.current_device():
+        _abi.check(fn(ctypes.byref(a), stream), what)
+    else:
+        with torch.cuda.device(device):
+            _abi.check(fn(ctypes.byref(a), stream), what)
 
 
 def qcache_write(c_cache, kr_cache, scales, c_kv, k_rope, *, gamma=None, rope_cos=None, rope_sin=None, start=None,
@@ -419,12 +443,11 @@ def qcache_write(c_cache, kr_cache, scales, c_kv, k_rope, *, gamma=None, rope_co
         _same(rope_sin, "rope_sin", (max_pos, d_rope // 2), torch.float32)
     if workspace is None:
         workspace = torch.empty(256, dtype=torch.uint8, device=c_kv.device)
-    a = _abi.QcacheWriteArgs(B, L, T_max, d_c, d_rope, int(scale_block), _dtype(c_kv), float(rms_eps), max_pos,
-                             _ptr(c_kv), _ptr(gamma), _ptr(k_rope), _ptr(rope_cos), _ptr(rope_sin), _ptr(start),
-                             _ptr(lens), _ptr(c_cache), _ptr(kr_cache), _ptr(scales), _ptr(workspace),
-                             workspace.numel() * workspace.element_size())
-    _call(_lib().gdla_qcache_write, a, (c_cache, kr_cache, scales, c_kv, k_rope, gamma, rope_cos, rope_sin, start, lens,
-                                        workspace), stream, "gdla_qcache_write")
+    dev = c_cache.get_device()
+    a = _abi.QcacheWriteArgs(B, L, T_max, d_c, d_rope, scale_block, _dtype(c_kv), rms_eps, max_pos,
+                             *_ptrs(dev, c_kv, gamma, k_rope, rope_cos, rope_sin, start, lens, c_cache, kr_cache, scales,
+                                    workspace), workspace.nbytes)
+    _call(_lib().gdla_qcache_write, a, dev, stream, "gdla_qcache_write")
 
 
 def _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out, n_kv=0,
@@ -433,17 +456,18 @@ def _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dt
     if dtype not in _DT:
         raise ValueError(f"unsupported dtype {dtype}; GDLA takes bfloat16 or float32")
     _same(lens, "lens", (B,), torch.int32)
-    dev = c_cache.device
+    dev = c_cache.get_device()
     if c_hat_out is None:
-        c_hat_out = torch.empty((B, length, d_c), dtype=dtype, device=dev)
+        c_hat_out = torch.empty((B, length, d_c), dtype=dtype, device=c_cache.device)
+    else:
+        _same(c_hat_out, "c_hat_out", (B, length, d_c), dtype)
     if k_rope_out is None:
-        k_rope_out = torch.empty((B, length, d_rope), dtype=dtype, device=dev)
-    _same(c_hat_out, "c_hat_out", (B, length, d_c), dtype)
-    _same(k_rope_out, "k_rope_out", (B, length, d_rope), dtype)
-    a = _abi.QcacheReadArgs(B, int(length), T_max, int(first), d_c, d_rope, int(scale_block), n_kv, d_nope, d_v,
-                            _DT[dtype], _ptr(c_cache), _ptr(kr_cache), _ptr(scales), _ptr(lens), _ptr(w_ukv),
-                            _ptr(c_hat_out), _ptr(k_rope_out), _ptr(kv_out))
-    return a, c_hat_out, k_rope_out
+        k_rope_out = torch.empty((B, length, d_rope), dtype=dtype, device=c_cache.device)
+    else:
+        _same(k_rope_out, "k_rope_out", (B, length, d_rope), dtype)
+    a = _abi.QcacheReadArgs(B, length, T_max, first, d_c, d_rope, scale_block, n_kv, d_nope, d_v, _DT[dtype],
+                            *_ptrs(dev, c_cache, kr_cache, scales, lens, w_ukv, c_hat_out, k_rope_out, kv_out))
+    return a, dev, c_hat_out, k_rope_out
 
 
 def qcache_read(c_cache, kr_cache, scales, *, length: int, first: int = 0, lens=None, scale_block: int = 1,
@@ -452,8 +476,8 @@ def qcache_read(c_cache, kr_cache, scales, *, length: int, first: int = 0, lens=
     ``dtype`` values: (c_hat [B,length,d_c], k_rope [B,length,d_rope]). With
     ``lens`` (int32 [B] on the device) only the first lens[b] of them are read;
     the others are zeros."""
-    a, c, k = _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out)
-    _call(_lib().gdla_qcache_read, a, (c_cache, kr_cache, scales, lens, c, k), stream, "gdla_qcache_read")
+    a, dev, c, k = _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out)
+    _call(_lib().gdla_qcache_read, a, dev, stream, "gdla_qcache_read")
     return c, k
 
 
@@ -464,13 +488,15 @@ def qcache_expand(c_cache, kr_cache, scales, w_ukv, *, n_kv: int, d_nope: int, d
     [B,length,d_rope], c_hat [B,length,d_c]). The key side of attend() over a
     cached prefix."""
     dtype = w_ukv.dtype
+    shape = (c_cache.shape[0], length, n_kv, d_nope + d_v)
     _same(w_ukv, "w_ukv", (c_cache.shape[-1], n_kv * (d_nope + d_v)))
     if kv_out is None:
-        kv_out = torch.empty((c_cache.shape[0], length, n_kv, d_nope + d_v), dtype=dtype, device=c_cache.device)
-    _same(kv_out, "kv_out", (c_cache.shape[0], length, n_kv, d_nope + d_v), dtype)
-    a, c, k = _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out,
-                           n_kv, d_nope, d_v, w_ukv, kv_out)
-    _call(_lib().gdla_qcache_expand, a, (c_cache, kr_cache, scales, lens, w_ukv, c, k, kv_out), stream, "gdla_qcache_expand")
+        kv_out = torch.empty(shape, dtype=dtype, device=c_cache.device)
+    else:
+        _same(kv_out, "kv_out", shape, dtype)
+    a, dev, c, k = _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out,
+                                n_kv, d_nope, d_v, w_ukv, kv_out)
+    _call(_lib().gdla_qcache_expand, a, dev, stream, "gdla_qcache_expand")
     return kv_out, k, c
 
 
@@ -502,18 +528,18 @@ def qcache_decode(c_cache, kr_cache, scales, q, w_ukv, rope_cos, rope_sin, lam_l
     _same(rope_sin, "rope_sin", (rope_cos.shape[0], d_rope // 2), torch.float32)
     if out is None:
         out = torch.empty((B, g * n_kv, d_v), dtype=q.dtype, device=q.device)
-    _same(out, "out", (B, g * n_kv, d_v), q.dtype)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    a = _abi.QcacheDecodeArgs(B, T_max, d_c, d_rope, n_kv, d_nope, d_v, n_kv, g, int(scale_block), _mask(mask),
-                              int(window), float(softmax_scale), _dtype(q), rope_cos.shape[0], _ptr(seqlens),
-                              _ptr(c_cache), _ptr(kr_cache), _ptr(scales), _ptr(q), _ptr(w_ukv), _ptr(rope_cos),
-                              _ptr(rope_sin), _ptr(lam_logits), _ptr(gate_logits), _ptr(out), _ptr(workspace), ws_bytes)
+    else:
+        _same(out, "out", (B, g * n_kv, d_v), q.dtype)
+    dev = c_cache.get_device()
     if workspace is None:
-        need = int(_lib().gdla_qcache_decode_workspace_size(ctypes.byref(a)))
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), need
-    _call(_lib().gdla_qcache_decode, a, (c_cache, kr_cache, scales, q, w_ukv, rope_cos, rope_sin, lam_logits, gate_logits,
-                                         seqlens, out, workspace), stream, "gdla_qcache_decode")
+        workspace = torch.empty(qcache_decode_workspace_size(B=B, T_max=T_max, d_c=d_c, d_rope=d_rope, n_kv=n_kv,
+                                                             d_nope=d_nope, d_v=d_v, g=g, dtype=q.dtype),
+                                dtype=torch.uint8, device=q.device)
+    a = _abi.QcacheDecodeArgs(B, T_max, d_c, d_rope, n_kv, d_nope, d_v, n_kv, g, scale_block, _mask(mask), window,
+                              softmax_scale, _dtype(q), rope_cos.shape[0],
+                              *_ptrs(dev, seqlens, c_cache, kr_cache, scales, q, w_ukv, rope_cos, rope_sin, lam_logits,
+                                     gate_logits, out, workspace), workspace.nbytes)
+    _call(_lib().gdla_qcache_decode, a, dev, stream, "gdla_qcache_decode")
     return out
 
 

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/gdla.h"
 
 namespace gdla {
@@ -144,7 +146,7 @@ cudaError_t launch_qcache_read(const QcacheReadParams& p, gdla_dtype dt, cudaStr
 // heads, then the heads' scales).
 constexpr int kQdecHeads = 48;
 constexpr int kQdecTile = 128;
-constexpr int kQdecPrefetch = 2;  // tiles prefetched into L2 ahead of the ring
+constexpr int kQdecPrefetch = 0;  // tiles prefetched into L2 ahead of the ring
 constexpr int kQdecSMs = 148;     // B200
 __host__ __device__ constexpr int qdec_image_data(int heads) { return 2 * heads * 576; }
 __host__ __device__ constexpr int qdec_image_bytes(int heads) { return (qdec_image_data(heads) + 4 * heads + 255) / 256 * 256; }
@@ -153,6 +155,18 @@ struct QdecodeParams {
   const float* scales;
   int sl, n_blocks;
 };
+// Allows a kernel `bytes` of dynamic shared memory, once a device (`done`: one bit each)
+template <typename K>
+cudaError_t allow_smem(K k, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 cudaError_t launch_qdecode_split_simt(const QdecodeParams& p, cudaStream_t s);
 // absorb, split and combine (bf16, d_c = 512, d_rope = 64, heads of 128)
 cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s);

@@ -1111,9 +1111,10 @@ __global__ void __launch_bounds__(q8::CB_T, 1)
 // ---------------------------------------------------------------- launches
 namespace {
 
-template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*k)(P...), dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <auto K, typename... A>
+cudaError_t launch_dependent(dim3 grid, int threads, int smem, cudaStream_t s, A... args) {
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(K, smem, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
@@ -1125,7 +1126,7 @@ cudaError_t launch_dependent(void (*k)(P...), dim3 grid, int threads, int smem, 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, args...);
+  return cudaLaunchKernelEx(&cfg, K, args...);
 }
 
 bool w_map(CUtensorMap* m, const DecodeParams& d, uint32_t rows) {
@@ -1150,7 +1151,8 @@ cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s) {
     a.isc = d.scale * kLog2e;
     a.q = reinterpret_cast<const __nv_bfloat16*>(d.q); a.seqlens = d.seqlens; a.cos_tab = d.cos_tab;
     a.sin_tab = d.sin_tab; a.qimg = d.qimg; a.status = d.status;
-    cudaError_t e = cudaFuncSetAttribute(qdecode_absorb_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, AB_SMEM);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(qdecode_absorb_kernel, AB_SMEM, allowed);
     if (e != cudaSuccess) return e;
     const int rows = d.B * (d.g + 1);
     qdecode_absorb_kernel<<<dim3((unsigned)d.n_kv, (unsigned)((rows + AB - 1) / AB), DC / AB), 256, AB_SMEM, s>>>(tw, a);
@@ -1176,9 +1178,9 @@ cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s) {
     const dim3 grid((unsigned)d.n_hg, (unsigned)d.n_ranges);
     cudaError_t e;
     switch (d.part_heads / HT) {
-      case 1: e = launch_dependent(qdecode_split_kernel<1>, grid, Lay<1>::NT, Lay<1>::SMEM, s, tc, tr, a); break;
-      case 2: e = launch_dependent(qdecode_split_kernel<2>, grid, Lay<2>::NT, Lay<2>::SMEM, s, tc, tr, a); break;
-      case 3: e = launch_dependent(qdecode_split_kernel<3>, grid, Lay<3>::NT, Lay<3>::SMEM, s, tc, tr, a); break;
+      case 1: e = launch_dependent<qdecode_split_kernel<1>>(grid, Lay<1>::NT, Lay<1>::SMEM, s, tc, tr, a); break;
+      case 2: e = launch_dependent<qdecode_split_kernel<2>>(grid, Lay<2>::NT, Lay<2>::SMEM, s, tc, tr, a); break;
+      case 3: e = launch_dependent<qdecode_split_kernel<3>>(grid, Lay<3>::NT, Lay<3>::SMEM, s, tc, tr, a); break;
       default: return cudaErrorInvalidValue;
     }
     if (e != cudaSuccess) return e;
@@ -1194,8 +1196,8 @@ cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s) {
   const int per_group = kQdecSMs / d.n_kv > 1 ? kQdecSMs / d.n_kv : 1;
   const int fill = (d.B + per_group - 1) / per_group, cap = CB_R / (d.g + 1);
   a.spb = fill < 1 ? 1 : (fill > cap ? cap : fill);
-  return launch_dependent(qdecode_combine_kernel, dim3((unsigned)d.n_kv, (unsigned)((d.B + a.spb - 1) / a.spb)), CB_T,
-                          CB_SMEM, s, tw, a);
+  return launch_dependent<qdecode_combine_kernel>(dim3((unsigned)d.n_kv, (unsigned)((d.B + a.spb - 1) / a.spb)), CB_T, CB_SMEM,
+                                                  s, tw, a);
 }
 
 }  // namespace gdla
