@@ -870,8 +870,8 @@ gdla_status gdla_qcache_decode(const gdla_qcache_decode_args* a, void* stream) {
   d.status = (int*)(ws + lay.status);
   p.scales = a->scales; p.sl = qcache_sl(a->scale_block);
   p.n_blocks = gdla_qcache_scale_blocks(a->T_max, a->scale_block);
+  if (lay.tc) return cuda_status(launch_qdecode_tc(p, s));  // (which clears the status word itself)
   cudaError_t e = cudaMemsetAsync(d.status, 0, kStatusBytes, s);
-  if (e == cudaSuccess && lay.tc) return cuda_status(launch_qdecode_tc(p, s));
   if (e == cudaSuccess) e = launch_decode_absorb(d, a->dtype, s);
   if (e == cudaSuccess) e = launch_qdecode_split_simt(p, s);
   if (e == cudaSuccess) e = launch_decode_combine(d, a->dtype, s);

@@ -104,6 +104,13 @@ __device__ __forceinline__ SeqTiles seq_tiles(const Args& a, int b) {
   s.n = (int)(((long long)s.Tb + TT - 1) / TT) - s.jt0;
   return s;
 }
+// lengths outside [0, T_max] are clamped, and reported
+__device__ __forceinline__ void report_lengths(const Args& a, int t, int nt) {
+  for (int b = t; b < a.B; b += nt) {
+    const int raw = __ldg(a.seqlens + b);
+    if (raw < 0 || raw > a.T_max) atomicCAS(a.status, 0, (int)GDLA_ERR_INVALID_ARG);
+  }
+}
 struct Walker {
   const Args* a;
   int b;
@@ -224,17 +231,11 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
     grid_dep_wait();
     return;
   }
-  if (earlier_failure(a.status)) {
-    grid_dep_wait();
-    return;
-  }
 
   // ---- this CTA's share of the W tiles, and the sequence that holds its first tile
   {
     long long loc = 0;
     for (int b = tid; b < a.B; b += NT) {
-      const int raw = __ldg(a.seqlens + b);
-      if ((raw < 0 || raw > a.T_max) && r == 0 && hg == 0) atomicCAS(a.status, 0, (int)GDLA_ERR_INVALID_ARG);
       loc += seq_tiles(a, b).n;
     }
     for (int o = 16; o; o >>= 1) loc += __shfl_xor_sync(0xffffffffu, loc, o);
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
   const int R = sh.R;
   if (start >= end || sh.b0 < 0) {  // a range beyond the tiles
     grid_dep_wait();                // (this grid never completes before the one it overlaps)
+    if (r == 0 && hg == 0) report_lengths(a, tid, NT);
     return;
   }
   const int b0 = sh.b0;
@@ -425,12 +427,13 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
     }
   } else if (warp == 2) {
     // -------------------------------------------------------- query images
+    grid_dep_wait();  // the absorb kernel wrote them, and cleared the status word
+    if (r == 0 && hg == 0) report_lengths(a, lane, 32);
     if (lane == 0) {
       Walker w;
       w.init(a, b0, p0);
       bool ok = true;
       int seg = 0;
-      grid_dep_wait();  // the absorb kernel wrote them
       for (long long t = start; t < end && ok; ++seg) {
         w.seek(t);
         if (seg > 0) ok = mbar_wait(smem_u32(&sh.q_free), (seg - 1) & 1, a.status, 531, &abort_flag);
@@ -663,7 +666,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
 // KV group h and 128 query rows (row = (sequence b, head u of the group)) a cluster of four
 // CTAs computes the 512 latent columns, 128 each, on the tensor cores; the largest magnitude
 // of a row is exchanged through distributed shared memory, so that the row is scaled by one
-// power of two and written once. The first CTA adds the rotary part.
+// power of two and written once. Each CTA adds a quarter of the rotary part.
 namespace q8 {
 constexpr int AB = 128;
 constexpr int AB_OP = AB * AB * 2;  // an operand: two 64-column chunks of [128 rows x 128 B]
@@ -683,24 +686,31 @@ __device__ __forceinline__ int image_offset(int NH, int row, int d) {
   return d < DC ? (d >> 7) * (2 * NH * 128) + row * 128 + ((((d & 127) >> 4) ^ (row & 7)) << 4) + (d & 15)
                 : 4 * (2 * NH * 128) + row * 64 + ((((d - DC) >> 4) ^ ((row >> 1) & 3)) << 4) + (d & 15);
 }
-// 16 values (already divided by the row's scale) into the hi and lo rows
+// values (already divided by the row's scale) into the hi and lo rows
+__device__ __forceinline__ void split4(const float* x, uint32_t& hi, uint32_t& lo) {
+  uint32_t hh[2], ll[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    hh[u] = e4m3x2(x[2 * u], x[2 * u + 1]);
+    const float2 f = __half22float2(e4m3x2_to_half2(hh[u]));
+    ll[u] = e4m3x2((x[2 * u] - f.x) * 16.f, (x[2 * u + 1] - f.y) * 16.f);
+  }
+  hi = hh[0] | (hh[1] << 16);
+  lo = ll[0] | (ll[1] << 16);
+}
 __device__ __forceinline__ void store16(uint8_t* img, int NH, int head, int d, const float (&x)[16]) {
   uint32_t hi[4], lo[4];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    uint32_t hh[2], ll[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const float a = x[4 * q + 2 * u], b = x[4 * q + 2 * u + 1];
-      hh[u] = e4m3x2(a, b);
-      const float2 f = __half22float2(e4m3x2_to_half2(hh[u]));
-      ll[u] = e4m3x2((a - f.x) * 16.f, (b - f.y) * 16.f);
-    }
-    hi[q] = hh[0] | (hh[1] << 16);
-    lo[q] = ll[0] | (ll[1] << 16);
-  }
+  for (int q = 0; q < 4; ++q) split4(x + 4 * q, hi[q], lo[q]);
   *reinterpret_cast<uint4*>(img + image_offset(NH, head, d)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
   *reinterpret_cast<uint4*>(img + image_offset(NH, NH + head, d)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+}
+__device__ __forceinline__ void store8(uint8_t* img, int NH, int head, int d, const float (&x)[8]) {
+  uint32_t hi[2], lo[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) split4(x + 4 * q, hi[q], lo[q]);
+  *reinterpret_cast<uint2*>(img + image_offset(NH, head, d)) = make_uint2(hi[0], hi[1]);
+  *reinterpret_cast<uint2*>(img + image_offset(NH, NH + head, d)) = make_uint2(lo[0], lo[1]);
 }
 }  // namespace q8
 
@@ -708,6 +718,12 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
     qdecode_absorb_kernel(const __grid_constant__ CUtensorMap tmW, const q8::AbsorbArgs a) {
   using namespace sm100;
   using namespace q8;
+  // the call's status word, before any kernel of the call can report to it
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < kStatusBytes / 4) {
+    a.status[threadIdx.x] = 0;
+    __threadfence();
+  }
+  __syncwarp();
   grid_dep_launch();
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* as = smem;
@@ -778,16 +794,20 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
   const int rl = q4 * 32 + lane, R = r0 + rl;
   const bool real = R < rows;
   const int b = real ? R / G1 : 0, head = real ? head_of(R % G1) : 0;
-  // the rotary pairs (k, k + 32), k = 8c .. 8c + 7, at position seqlen - 1
-  const int pos = min(max(__ldg(a.seqlens + b), 1), a.T_max) - 1;
-  auto rope8 = [&](int c, float (&lo)[8], float (&hi)[8]) {
-    const __nv_bfloat16* qr = a.q + ((long long)b * a.H_q + head) * 192 + 128;
-    const uint4 xl = *reinterpret_cast<const uint4*>(qr + 8 * c);
-    const uint4 xh = *reinterpret_cast<const uint4*>(qr + 32 + 8 * c);
+  // this CTA's rotary pairs (k, k + 32), k = 8z .. 8z + 7, at position seqlen - 1
+  const bool rot = ch == 0 && real;
+  float lo[8], hi[8], mx = 0.f;
+  if (rot) {
+    const int pos = min(max(__ldg(a.seqlens + b), 1), a.T_max) - 1;
+    const __nv_bfloat16* qr = a.q + ((long long)b * a.H_q + head) * 192 + 128 + 8 * z;
+    const uint4 xl = *reinterpret_cast<const uint4*>(qr), xh = *reinterpret_cast<const uint4*>(qr + 32);
+    const float4* c4 = reinterpret_cast<const float4*>(a.cos_tab + (long long)pos * 32 + 8 * z);
+    const float4* s4 = reinterpret_cast<const float4*>(a.sin_tab + (long long)pos * 32 + 8 * z);
+    const float4 cq[2] = {__ldg(c4), __ldg(c4 + 1)}, sq[2] = {__ldg(s4), __ldg(s4 + 1)};
+    const float* cs = reinterpret_cast<const float*>(cq);
+    const float* sn = reinterpret_cast<const float*>(sq);
     const __nv_bfloat162* l2 = reinterpret_cast<const __nv_bfloat162*>(&xl);
     const __nv_bfloat162* h2 = reinterpret_cast<const __nv_bfloat162*>(&xh);
-    const float* cs = a.cos_tab + (long long)pos * 32 + 8 * c;
-    const float* sn = a.sin_tab + (long long)pos * 32 + 8 * c;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float2 x1 = __bfloat1622float2(l2[e]), x2 = __bfloat1622float2(h2[e]);
@@ -796,17 +816,8 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
       hi[2 * e] = (x2.x * cs[2 * e] + x1.x * sn[2 * e]) * a.isc;
       hi[2 * e + 1] = (x2.y * cs[2 * e + 1] + x1.y * sn[2 * e + 1]) * a.isc;
     }
-  };
-  const bool rot = z == 0 && ch == 0 && real;
-  float rmx = 0.f;
-  if (rot) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float lo[8], hi[8];
-      rope8(c, lo, hi);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) rmx = fmaxf(rmx, fmaxf(fabsf(lo[e]), fabsf(hi[e])));
-    }
+    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fmaxf(fabsf(lo[e]), fabsf(hi[e])));
   }
   const bool done = mbar_wait(smem_u32(&bar[1]), 0, a.status, 542);
   __syncwarp();
@@ -815,7 +826,6 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
   tmem_ld32(tmem + ((uint32_t)(q4 * 32) << 16) + ch * 64, v0);
   tmem_ld32(tmem + ((uint32_t)(q4 * 32) << 16) + ch * 64 + 32, v1);
   tmem_wait_ld();
-  float mx = rmx;
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
     v0[i] = __float_as_uint(__uint_as_float(v0[i]) * a.isc);
@@ -850,23 +860,14 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
       store16(img, NH, lh, z * AB + ch * 64 + 16 * c, x);
     }
     if (rot) {
-      *reinterpret_cast<float*>(img + img_data + 4 * lh) = __int_as_float((127 + ex) << 23);
+      if (z == 0) *reinterpret_cast<float*>(img + img_data + 4 * lh) = __int_as_float((127 + ex) << 23);
 #pragma unroll
-      for (int c2 = 0; c2 < 2; ++c2) {
-        float y[16];
-        float lo0[8], hi0[8], lo1[8], hi1[8];
-        rope8(2 * c2, lo0, hi0);
-        rope8(2 * c2 + 1, lo1, hi1);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = fmaf(lo0[e], inv, bad);
-          x[8 + e] = fmaf(lo1[e], inv, bad);
-          y[e] = fmaf(hi0[e], inv, bad);
-          y[8 + e] = fmaf(hi1[e], inv, bad);
-        }
-        store16(img, NH, lh, DC + 16 * c2, x);
-        store16(img, NH, lh, DC + 32 + 16 * c2, y);
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = fmaf(lo[e], inv, bad);
+        hi[e] = fmaf(hi[e], inv, bad);
       }
+      store8(img, NH, lh, DC + 8 * z, lo);
+      store8(img, NH, lh, DC + 32 + 8 * z, hi);
     }
   }
   // image rows of the padding heads of each head group are zero (their scale is 1): the blocks
@@ -903,7 +904,8 @@ namespace q8 {
 constexpr int CB_R = 32, CB_N = 128;
 constexpr int CB_A = 64 * DC * 2;        // 8 chunks of [64 rows x 128 B]
 constexpr int CB_B = DC * CB_N * 2;      // 2 MN blocks of [512 K rows x 128 B]
-constexpr int CB_SMEM = CB_A + CB_B + 64;
+constexpr int CB_W = CB_R * kQdecSMs * 4;  // weights of a row's partials
+constexpr int CB_SMEM = CB_A + CB_B + CB_W + 64;
 constexpr int CB_T = 512;
 struct CombineArgs {
   int B, T_max, n_kv, g, H_q, n_hg, hpc, NH, n_ranges, spb;
@@ -925,10 +927,10 @@ __global__ void __launch_bounds__(q8::CB_T, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* as = smem;         // O_lat; later H (fp32 [64 x 128])
   uint8_t* bs = smem + CB_A;  // W_UV,h
-  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + CB_A + CB_B);
+  float* wgt = reinterpret_cast<float*>(smem + CB_A + CB_B);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(smem + CB_A + CB_B + CB_W);
   __shared__ long long rec0[CB_R];
   __shared__ int n_parts[CB_R];
-  __shared__ float row_max[CB_R], row_inv[CB_R];
   __shared__ uint32_t tmem_slot;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (smem_u32(smem) & 1023u) {
@@ -957,6 +959,16 @@ __global__ void __launch_bounds__(q8::CB_T, 1)
     tmem_alloc(smem_u32(&tmem_slot), CB_N);
     tmem_relinquish();
   }
+  // lambda and the gate logits of this thread's eight outputs (inputs of the caller)
+  const int e_out = tid, n_out = nb * a.g * (CB_N / 8);  // (at most 32 x 16)
+  const int o_bl = e_out / (a.g * (CB_N / 8)), o_u = (e_out / (CB_N / 8)) % a.g, o_c = e_out % (CB_N / 8);
+  const long long o_idx = ((long long)(b0 + o_bl) * n_S + h * a.g + o_u) * CB_N + o_c * 8;
+  uint4 gv = make_uint4(0, 0, 0, 0);
+  float lamv = 0.f;
+  if (e_out < n_out) {
+    gv = *reinterpret_cast<const uint4*>(a.gate + o_idx);
+    lamv = sigmoidf_(__ldg(a.lam + (long long)(b0 + o_bl) * n_S + h * a.g + o_u));
+  }
   grid_dep_wait();  // the partials come from the split kernel
   if (tid < CB_R) {
     n_parts[tid] = 0;
@@ -975,25 +987,35 @@ __global__ void __launch_bounds__(q8::CB_T, 1)
     }
   }
   __syncthreads();
+  // weights of a row's partials: one warp per row
   for (int r = warp; r < R; r += CB_T / 32) {
     const int np = n_parts[r];
-    const long long r0 = rec0[r];
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + rec0[r];
+    float* wr = wgt + r * kQdecSMs;
+    constexpr int kPL = (kQdecSMs + 31) / 32;  // partials of a lane
+    float2 v[kPL];
     float M = -INFINITY;
-    for (int sp = lane; sp < np; sp += 32) M = fmaxf(M, a.part_ml[(r0 + sp * rstep) * 2]);
+#pragma unroll
+    for (int q = 0; q < kPL; ++q) {
+      v[q] = lane + 32 * q < np ? ml[(lane + 32 * q) * rstep] : make_float2(-INFINITY, 0.f);
+      M = fmaxf(M, v[q].x);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     float den = 0.f;
-    for (int sp = lane; sp < np; sp += 32) {
-      const float m = a.part_ml[(r0 + sp * rstep) * 2], l = a.part_ml[(r0 + sp * rstep) * 2 + 1];
+#pragma unroll
+    for (int q = 0; q < kPL; ++q) {
       // (a share whose every score was NaN has M = -inf and l = NaN, and passes it on)
-      den += m == -INFINITY ? l : exp2f(m - M) * l;
+      const float f = v[q].x == -INFINITY ? 1.f : exp2f(v[q].x - M);
+      den += f * v[q].y;
+      v[q].x = f;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-    if (lane == 0) {
-      row_max[r] = M;
-      row_inv[r] = den == 0.f ? 0.f : 1.f / den;
-    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+#pragma unroll
+    for (int q = 0; q < kPL; ++q)
+      if (lane + 32 * q < np) wr[lane + 32 * q] = v[q].x * inv;
   }
   __syncthreads();
   constexpr int kMB = 8;  // partials in flight per thread
@@ -1004,27 +1026,23 @@ __global__ void __launch_bounds__(q8::CB_T, 1)
     for (int q = 0; q < 8; ++q) acc[q] = 0.f;
     if (r < R) {
       const int np = n_parts[r];
-      const float M = row_max[r], inv = row_inv[r];
       const float* src = a.part_o + rec0[r] * DC + c8 * 8;
-      const float* mls = a.part_ml + rec0[r] * 2;
+      const float* wr = wgt + r * kQdecSMs;
       for (int sp0 = 0; sp0 < np; sp0 += kMB) {
         float4 x[kMB][2];
-        float wv[kMB];
 #pragma unroll
         for (int q = 0; q < kMB; ++q) {
           x[q][0] = x[q][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-          wv[q] = 0.f;
           if (sp0 + q < np) {
             const float4* s4 = reinterpret_cast<const float4*>(src + (sp0 + q) * rstep * DC);
             x[q][0] = s4[0];
             x[q][1] = s4[1];
-            wv[q] = mls[(sp0 + q) * rstep * 2];
           }
         }
 #pragma unroll
         for (int q = 0; q < kMB; ++q) {
           if (sp0 + q >= np) continue;
-          const float f = wv[q] == -INFINITY ? inv : exp2f(wv[q] - M) * inv;
+          const float f = wr[sp0 + q];
           acc[0] = fmaf(f, x[q][0].x, acc[0]); acc[1] = fmaf(f, x[q][0].y, acc[1]);
           acc[2] = fmaf(f, x[q][0].z, acc[2]); acc[3] = fmaf(f, x[q][0].w, acc[3]);
           acc[4] = fmaf(f, x[q][1].x, acc[4]); acc[5] = fmaf(f, x[q][1].y, acc[5]);
@@ -1079,28 +1097,21 @@ __global__ void __launch_bounds__(q8::CB_T, 1)
     }
   }
   __syncthreads();
-  if (done && !earlier_failure(a.status)) {
-    for (int e = tid; e < nb * a.g * (CB_N / 8); e += CB_T) {
-      const int bl = e / (a.g * (CB_N / 8)), u = (e / (CB_N / 8)) % a.g, c8 = e % (CB_N / 8);
-      const int b = b0 + bl, sh = h * a.g + u;
-      const float lamv = sigmoidf_(a.lam[(long long)b * n_S + sh]);
-      const long long idx = ((long long)b * n_S + sh) * CB_N + c8 * 8;
-      const uint4 gv = *reinterpret_cast<const uint4*>(a.gate + idx);
-      const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&gv);
-      const float* hsr = hs + (bl * G1 + u) * CB_N + c8 * 8;
-      const float* hnr = hs + (bl * G1 + a.g) * CB_N + c8 * 8;
-      uint32_t o[4];
+  if (e_out < n_out && done && !earlier_failure(a.status)) {
+    const __nv_bfloat162* g2 = reinterpret_cast<const __nv_bfloat162*>(&gv);
+    const float* hsr = hs + (o_bl * G1 + o_u) * CB_N + o_c * 8;
+    const float* hnr = hs + (o_bl * G1 + a.g) * CB_N + o_c * 8;
+    uint32_t o[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float2 gf = __bfloat1622float2(g2[q]);
-        float d[2];
+    for (int q = 0; q < 4; ++q) {
+      const float2 gf = __bfloat1622float2(g2[q]);
+      float d[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          d[i] = (hsr[2 * q + i] + hsr[CB_R * CB_N + 2 * q + i]) - lamv * (hnr[2 * q + i] + hnr[CB_R * CB_N + 2 * q + i]);
-        o[q] = pack_bf16x2(d[0] * sigmoidf_(gf.x), d[1] * sigmoidf_(gf.y));
-      }
-      *reinterpret_cast<uint4*>(a.out + idx) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int i = 0; i < 2; ++i)
+        d[i] = (hsr[2 * q + i] + hsr[CB_R * CB_N + 2 * q + i]) - lamv * (hnr[2 * q + i] + hnr[CB_R * CB_N + 2 * q + i]);
+      o[q] = pack_bf16x2(d[0] * sigmoidf_(gf.x), d[1] * sigmoidf_(gf.y));
     }
+    *reinterpret_cast<uint4*>(a.out + o_idx) = make_uint4(o[0], o[1], o[2], o[3]);
   }
   tc_fence_before();
   __syncthreads();
