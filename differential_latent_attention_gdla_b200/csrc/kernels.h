@@ -146,7 +146,6 @@ cudaError_t launch_qcache_read(const QcacheReadParams& p, gdla_dtype dt, cudaStr
 // heads, then the heads' scales).
 constexpr int kQdecHeads = 48;
 constexpr int kQdecTile = 128;
-constexpr int kQdecPrefetch = 0;  // tiles prefetched into L2 ahead of the ring
 constexpr int kQdecSMs = 148;     // B200
 __host__ __device__ constexpr int qdec_image_data(int heads) { return 2 * heads * 576; }
 __host__ __device__ constexpr int qdec_image_bytes(int heads) { return (qdec_image_data(heads) + 4 * heads + 255) / 256 * 256; }

@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "sm100.cuh"
 
 namespace gdla {
 
@@ -34,6 +35,9 @@ __global__ void __launch_bounds__(256) qdecode_split_simt_kernel(const QdecodePa
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const float sl2 = p.scale * kLog2e;
 
+  // (started while the absorb kernel still runs; the combine kernel in turn beside this one)
+  sm100::grid_dep_launch();
+  sm100::grid_dep_wait();
   for (int e = tid; e < H_q * d_c; e += 256) qa[e] = p.q_abs[(long long)b * H_q * d_c + e];
   for (int e = tid; e < H_q * d_r; e += 256) qr[e] = p.q_rot[(long long)b * H_q * d_r + e];
   for (int e = tid; e < H_q; e += 256) {
@@ -155,8 +159,17 @@ cudaError_t one(const QdecodeParams& p, cudaStream_t s) {
   auto k = qdecode_split_simt_kernel<HPT, CPT>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  k<<<dim3((unsigned)d.n_splits, (unsigned)d.B), 256, smem, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)d.n_splits, (unsigned)d.B);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, p);
 }
 template <int HPT>
 cudaError_t by_width(const QdecodeParams& p, cudaStream_t s) {

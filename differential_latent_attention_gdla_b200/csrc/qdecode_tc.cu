@@ -24,11 +24,19 @@
 // A share writes one partial (M, l, O) per sequence it touches, to record r + b; the
 // combine kernel merges the records of a sequence.
 //
-// Block: warp 0 loads tiles (TMA, two stages of 72 KB released in halves, L2 prefetch ahead);
-// warp 1 issues the MMAs, warp 2 loads query images, warp 3 idles; the others are the
-// softmax, a group of four warps for each 16 of the up to 48 heads: a thread owns
-// one token (TMEM lane) and 16 heads, and the four warps of a group agree on their heads'
-// references by a barrier of their own. Every wait is bounded and reports GDLA_ERR_TIMEOUT.
+// Block: warp 0 loads tiles (TMA, two stages of 72 KB), warp 1 issues the MMAs, warp 2 loads
+// query images, warp 3 idles; the others are the softmax, a group of four warps for each 16 of
+// the up to 48 heads: a thread owns one token (TMEM lane) and 16 heads, and the four warps of
+// a group agree on their heads' references by a barrier of their own. Every wait is bounded
+// and reports GDLA_ERR_TIMEOUT.
+//
+// What bounds it (B=64 over 32768 tokens, 48 heads: 280 us replayed, 4.3 TB/s of cache): a
+// tile's way through its stage -- load, scores (1015 cycles of shared-memory reads), softmax
+// (~1750), values (905) -- with two of them in flight; the loads alone run at the memory's
+// rate (without the MMAs: 211 us). Tried and slower: prefetches into L2 (337 us a call without,
+// 344 to 363 with one to four tiles ahead), stages released in halves (the same) or quarters
+// (+5 %), box by box (+30 %: a row's 512 bytes are then read at four times), and three stages
+// of 96 tokens (+13 %: the softmax's work a tile is the same for fewer tokens).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -41,7 +49,6 @@ namespace q8 {
 
 constexpr int DC = 512, DR = 64;
 constexpr int TT = kQdecTile;                  // cache tokens per tile (M of the score MMA)
-constexpr int HALF = TT / 2;                   // tokens of a stage half
 constexpr int HT = 16;                         // heads per softmax thread
 constexpr int BOX = TT * 128, RBOX = TT * 64;  // a 128-column box of the tile; the rotary box
 constexpr int TILE = 4 * BOX + RBOX;
@@ -60,7 +67,7 @@ struct Lay {
   static constexpr int OFF_TILES = QIMG, OFF_P = OFF_TILES + STAGES * TILE, OFF_SH = OFF_P + PBYTES;
   static constexpr int NSW = 4 * HG, NT = 32 * (4 + NSW);  // softmax warps; threads
   struct Shared {
-    uint64_t full[STAGES], empty[2 * STAGES];
+    uint64_t full[STAGES], empty[STAGES];
     uint64_t s_full, s_free, p_full, p_free;
     uint64_t q_full, q_free, seg_done, mma_done;
     uint32_t tmem_slot;
@@ -187,20 +194,17 @@ __device__ __forceinline__ void score_mmas(uint32_t smem, uint32_t tmem) {
   for (int kk = 0; kk < 2; ++kk) mma_f8_ss(tmem + COL_S, c64 + 2 * kk, q64 + 2 * kk, id, 1);
 }
 template <int HG, int ST>
-__device__ __forceinline__ void value_mmas(uint32_t smem, uint32_t tmem, uint32_t acc, uint32_t empty0) {
+__device__ __forceinline__ void value_mmas(uint32_t smem, uint32_t tmem, uint32_t acc) {
   using namespace sm100;
   using L = Lay<HG>;
   constexpr uint32_t id = idesc_f8_f32(128, L::NQ, kF8E4m3, kF8E4m3, true, true);
   const uint64_t c = sdesc_sw128(smem + L::OFF_TILES + ST * TILE, BOX, 1024);
   const uint64_t wd = sdesc_sw128(smem + L::OFF_P, BOX, 1024);
 #pragma unroll
-  for (int kk = 0; kk < TT / 32; ++kk) {  // 32 tokens: 4096 bytes of a box and of the weights
+  for (int kk = 0; kk < TT / 32; ++kk)  // 32 tokens: 4096 bytes of a box and of the weights
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
       mma_f8_ss(tmem + L::NQ * (1 + mt), c + ((mt * BOX + kk * 4096) >> 4), wd + ((kk * 4096) >> 4), id, kk ? 1u : acc);
-    // the stage's halves go back to the producer one by one
-    if (kk == TT / 64 - 1) mma_commit(empty0);
-  }
 }
 
 }  // namespace q8
@@ -293,8 +297,10 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
   const int nh = min(a.hpc, a.H_q - hg * a.hpc);  // query heads of this head group
 
   if (tid == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(smem_u32(&sh.full[i]), 1);
-    for (int i = 0; i < 2 * STAGES; ++i) mbar_init(smem_u32(&sh.empty[i]), 1);
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), 1);
+    }
     mbar_init(smem_u32(&sh.s_full), 1);
     mbar_init(smem_u32(&sh.s_free), NSW);
     mbar_init(smem_u32(&sh.p_full), NSW);
@@ -320,21 +326,11 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ producer
     if (lane == 0) {
-      Walker wl, wp;  // the ring loads, and the L2 prefetches kQdecPrefetch tiles ahead of them
+      Walker wl;
       wl.init(a, b0, p0);
-      wp.init(a, b0, p0);
-      auto prefetch = [&](long long t) {
-        wp.seek(t);
-        const int j = wp.token0(t), rows = min(TT, a.T_max - j);
-        const long long row0 = (long long)wp.b * a.T_max + j;
-        bulk_prefetch_l2(a.c8 + row0 * DC, (uint32_t)rows * DC);
-        bulk_prefetch_l2(a.kr8 + row0 * DR, (uint32_t)rows * DR);
-      };
-      for (int k = STAGES; k < STAGES + kQdecPrefetch && k < n_tiles; ++k) prefetch(start + k);
       int k = 0;
       for (; k < n_tiles && !abort_flag; ++k) {
         const int st = k % STAGES;
-        if (k >= STAGES && k + kQdecPrefetch < n_tiles) prefetch(start + k + kQdecPrefetch);
         const long long t = start + k;
         wl.seek(t);
         if (t == wl.pb && hg == 0)  // this CTA holds the sequence's first tile: record who covers it
@@ -342,21 +338,14 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
         const int j0 = wl.token0(t);
         const uint32_t bar = smem_u32(&sh.full[st]);
         const uint32_t dst = smem_u32(tiles + st * TILE);
-        bool ok = true;
-        for (int hf = 0; hf < 2 && ok; ++hf) {
-          if (k >= STAGES)
-            ok = mbar_wait(smem_u32(&sh.empty[2 * st + hf]), ((k / STAGES) & 1) ^ 1, a.status, 501, &abort_flag);
-          if (!ok) break;
-          if (hf == 0) mbar_expect_tx(bar, TILE);
-          for (int bx = 0; bx < 4; ++bx)
-            tma_load_3d(dst + bx * BOX + hf * (BOX / 2), &tmC, bar, bx * 128, j0 + HALF * hf, wl.b);
-          tma_load_3d(dst + 4 * BOX + hf * (RBOX / 2), &tmR, bar, 0, j0 + HALF * hf, wl.b);
-        }
-        if (!ok) {
+        if (k >= STAGES &&
+            !mbar_wait(smem_u32(&sh.empty[st]), ((k / STAGES) & 1) ^ 1, a.status, 501, &abort_flag)) {
           abort_flag = 1;
-          ++k;  // (the tile's first half may be on its way)
           break;
         }
+        mbar_expect_tx(bar, TILE);
+        for (int bx = 0; bx < 4; ++bx) tma_load_3d(dst + bx * BOX, &tmC, bar, bx * 128, j0, wl.b);
+        tma_load_3d(dst + 4 * BOX, &tmR, bar, 0, j0, wl.b);
       }
       if (abort_flag)
         for (int q = (k > STAGES ? k - STAGES : 0); q < k; ++q)
@@ -401,10 +390,10 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
           const uint32_t acc = kv > 0 && t != wv.pb;
           tc_fence_after();
           if (kv & 1)
-            value_mmas<HG, 1>(smem_u32(smem), tmem, acc, smem_u32(&sh.empty[2]));
+            value_mmas<HG, 1>(smem_u32(smem), tmem, acc);
           else
-            value_mmas<HG, 0>(smem_u32(smem), tmem, acc, smem_u32(&sh.empty[0]));
-          mma_commit(smem_u32(&sh.empty[2 * (kv % STAGES) + 1]));
+            value_mmas<HG, 0>(smem_u32(smem), tmem, acc);
+          mma_commit(smem_u32(&sh.empty[kv % STAGES]));
           mma_commit(smem_u32(&sh.p_free));
           if (kv == n_tiles - 1 || t == wv.pb + wv.st.n - 1) mma_commit(smem_u32(&sh.seg_done));  // O^T holds the share
           ++kv;
@@ -1174,10 +1163,10 @@ cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s) {
     CUtensorMap tc, tr;
     const uint64_t cd[3] = {(uint64_t)DC, (uint64_t)d.T_max, (uint64_t)d.B};
     const uint64_t cs[2] = {(uint64_t)DC, (uint64_t)d.T_max * DC};
-    const uint32_t cb[3] = {128, (uint32_t)HALF, 1};
+    const uint32_t cb[3] = {128, (uint32_t)TT, 1};
     const uint64_t rd[3] = {(uint64_t)DR, (uint64_t)d.T_max, (uint64_t)d.B};
     const uint64_t rs[2] = {(uint64_t)DR, (uint64_t)d.T_max * DR};
-    const uint32_t rb[3] = {64, (uint32_t)HALF, 1};
+    const uint32_t rb[3] = {64, (uint32_t)TT, 1};
     if (!make_tmap_u8(&tc, d.c_cache, 3, cd, cs, cb, 128) || !make_tmap_u8(&tr, d.kr_cache, 3, rd, rs, rb, 64))
       return cudaErrorInvalidValue;
     Args a{};
