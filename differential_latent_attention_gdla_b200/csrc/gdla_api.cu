@@ -296,8 +296,12 @@ int qcache_sl(int scale_block) {
   return -1;
 }
 
+// (the kernels' positions run up to a tile or a block past the last token in 32 bits)
+constexpr int kQcacheMaxTokens = 0x7FFFFFFF - 1024;
+
 gdla_status qcache_dims(int B, int T_max, int d_c, int d_rope, int scale_block, int dtype) {
   if (B < 1 || B > 65535 || T_max < 1 || qcache_sl(scale_block) < 0) return GDLA_ERR_INVALID_ARG;
+  if (T_max > kQcacheMaxTokens) return GDLA_ERR_UNSUPPORTED;
   if (dtype != GDLA_BF16 && dtype != GDLA_FP32) return GDLA_ERR_INVALID_ARG;
   if (!latent_ok(d_c) || (d_rope != 16 && d_rope != 32 && d_rope != 64)) return GDLA_ERR_UNSUPPORTED;
   return GDLA_OK;
@@ -821,6 +825,7 @@ static gdla_status validate_qdecode(const gdla_qcache_decode_args* a) {
                                a->dtype);
   if (st != GDLA_OK) return st;
   if (qcache_sl(a->scale_block) < 0) return GDLA_ERR_INVALID_ARG;
+  if (a->T_max > kQcacheMaxTokens) return GDLA_ERR_UNSUPPORTED;
   const gdla_decode_args shape = qdecode_shape(a);
   // (the tensor-core path's heads are 128 wide: d_rope = 64 admits no others.) The CUDA-core
   // split kernel holds every query head of a sequence in one block

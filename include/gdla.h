@@ -346,14 +346,16 @@ gdla_status gdla_gates(const gdla_gates_args* args, void* stream);
  * patterns included, and so may their scales.
  *
  * Supported: d_c in {64, 128, 256, 512}, d_rope in {16, 32, 64} for write and read;
- * the head shapes of the other entry points for expand and decode. */
+ * the head shapes of the other entry points for expand and decode; T_max up to
+ * 2^31 - 1025. */
 
 /* Scales of one sequence: ceil(T_max / scale_block); 0 for an invalid size. */
 int gdla_qcache_scale_blocks(int T_max, int scale_block);
 
 /* Writes the rows of new tokens: latent RMSNorm, RoPE of the rotary key at the
- * token's position (both as in gdla_latent_expand, kept in fp32 or more until the
- * one rounding to 8 bits), quantisation, store. Sequence b's tokens
+ * token's position (both as in gdla_latent_expand, in fp32 until the one rounding
+ * to 8 bits; which scale a block takes is decided in 64 bits where fp32 cannot tell),
+ * quantisation, store. Sequence b's tokens
  * 0 .. lens[b]-1 of the [B, L] inputs go to positions start[b] .. start[b]+lens[b]-1
  * (a prompt, a chunk behind a cached prefix, or the single token of a decode step).
  *  - gamma == NULL: c_kv and k_rope are rows already normalised and rotated (the

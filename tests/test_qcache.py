@@ -61,11 +61,12 @@ def good_decode():
 def sets(**kw):
     def mut(a):
         for k, v in kw.items():
-            setattr(a, k, v)
+            if hasattr(a, k):
+                setattr(a, k, v)
     return mut
 
 
-DIMS = [(sets(B=0), E), (sets(B=65536), E), (sets(T_max=0), E), (sets(scale_block=0), E), (sets(scale_block=3), E),
+DIMS = [(sets(T_max=0x7FFFFFFF, rope_max_pos=0x7FFFFFFF), U), (sets(B=0), E), (sets(B=65536), E), (sets(T_max=0), E), (sets(scale_block=0), E), (sets(scale_block=3), E),
         (sets(scale_block=256), E), (sets(scale_block=-1), E), (sets(dtype=2), E), (sets(d_c=500), U),
         (sets(d_rope=48), U), (sets(c_cache=0), E), (sets(kr_cache=BASE + 8), E), (sets(scales=BASE + 4), E)]
 

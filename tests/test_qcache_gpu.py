@@ -103,7 +103,17 @@ WRITES = [
 ]
 
 
-@pytest.mark.parametrize("d_c,d_rope,dt,T,L,nb,start,lens", WRITES)
+# the kernel of many bf16 tokens (16384 and more): chunks of whole blocks, ragged at both ends
+MANY = [
+    (512, 64, "bf16", 7000, 6000, 1, [0, 999, 1000], [6000, 5990, 0]),
+    (512, 64, "bf16", 7000, 6000, 16, [5, 1000, 37], [5999, 6000, 5000]),
+    (512, 64, "bf16", 7000, 6000, 64, [63, 64, 65], [6000, 1, 5937]),
+    (256, 32, "bf16", 7000, 6000, 2, [1, 0, 77], [6000, 6000, 3]),
+    (64, 16, "bf16", 7000, 6000, 32, [0, 31, 1000], [5985, 6000, 6000]),
+]
+
+
+@pytest.mark.parametrize("d_c,d_rope,dt,T,L,nb,start,lens", WRITES + MANY)
 @pytest.mark.parametrize("norm", [True, False])
 def test_write(d_c, d_rope, dt, T, L, nb, start, lens, norm):
     B, gen, dtype = 3, gen_for(T * 131 + L), DT[dt]
@@ -169,10 +179,38 @@ def test_write_scale_borders_and_extremes():
     assert (f64(sc)[0] == want).all()
 
 
+@pytest.mark.parametrize("dt,B,L", [("bf16", 1, 64), ("fp32", 1, 64), ("bf16", 3, 6000)])
+def test_write_scales_next_to_their_borders(dt, B, L):
+    # normalised maxima within 1e-6 of 448 2^e = 0.875 on either side: rows of equal magnitudes a
+    # give gamma / sqrt(1 + eps / a^2), and a last element a little larger or smaller moves it
+    gen = gen_for(60)
+    a = torch.exp2(torch.randint(-3, 12, (B, L, 1), generator=gen).float())
+    c = a * (torch.randint(0, 2, (B, L, 64), generator=gen) * 2 - 1)
+    if dt == "fp32":
+        c[..., -1] *= 1 + 2.0 ** -20 * torch.randint(-8, 9, (B, L), generator=gen)
+    else:  # (one larger element among the small ones; the gain makes up for it)
+        c[..., -1] *= 1 + 2.0 ** -7 * torch.randint(0, 2, (B, L), generator=gen)
+    c = c.to(DT[dt])
+    gamma = torch.full((64,), 0.875).to(DT[dt])
+    gamma[-1] = 0.5
+    k = torch.zeros((B, L, 16), dtype=DT[dt])
+    cos, sin = gdla.rope_tables(L, 16, device=DEV)
+    cache = gdla.qcache_empty(B, L, d_c=64, d_rope=16, device=DEV)
+    gdla.qcache_write(*cache, c.to(DEV), k.to(DEV), gamma=gamma.to(DEV), rope_cos=cos, rope_sin=sin)
+    x = f64(c)
+    x = x / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6) * f64(gamma)
+    top = np.abs(x).max(-1)
+    want = np.where(top <= 0.875, 2.0 ** -9, 2.0 ** -8)
+    assert (np.abs(top - 0.875) < 1e-3).all() and (want == 2.0 ** -9).any()
+    assert (f64(cache[2]) == want).all()
+    assert_quantised(e4m3_values(cache[0]), x, want[..., None])
+
+
+@pytest.mark.parametrize("T", [40, 16400])
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
-def test_write_not_finite_values_stay_apart(dt):
+def test_write_not_finite_values_stay_apart(dt, T):
     # a NaN or infinity is stored as NaN; the rest of the row, and its block, as without it
-    gen, T, nb = gen_for(5), 40, 8
+    gen, nb = gen_for(5), 8
     c = torch.randn((1, T, 64), generator=gen).to(DT[dt])
     k = torch.randn((1, T, 16), generator=gen).to(DT[dt])
     bad = [(3, 7, float("nan")), (12, 0, float("inf")), (30, 63, float("-inf"))]
@@ -196,7 +234,7 @@ def test_write_not_finite_values_stay_apart(dt):
     assert torch.equal(got, ref)
     sc = f64(clean[2])[0]
     sc_d = f64(dirty[2])[0]
-    keep = [b for b in range(5) if b != 20 // nb]  # (the rotary value was a number before)
+    keep = [b for b in range(T // nb) if b != 20 // nb]  # (the rotary value was a number before)
     assert (sc_d[keep] == sc[keep]).all()
 
 
