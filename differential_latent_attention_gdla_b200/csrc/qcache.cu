@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(512, 2) qcache_write_bulk_kernel(const QcacheW
   const float inv_dc = (512 / p.d_c) * 0x1p-9f;  // (d_c divides 512)
   const int cnt = hi - lo;
   __syncthreads();
-  bool landed = false;
+  bool landed = false, failed = false;
   // a warp's tokens four at a time, each step for all four: their latencies overlap
   for (int i0 = warp; i0 < cnt; i0 += nw * kBulkBatch) {
     float k1[kBulkBatch], k2[kBulkBatch], cs[kBulkBatch], sn[kBulkBatch], ss[kBulkBatch], mx[kBulkBatch];
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(512, 2) qcache_write_bulk_kernel(const QcacheW
         }
       }
     }
-    if (!landed) landed = sm100::mbar_wait(sm100::smem_u32(&bar), 0, p.status, 561);
+    if (!landed) failed = !(landed = sm100::mbar_wait(sm100::smem_u32(&bar), 0, p.status, 561));
     __syncwarp();
 #pragma unroll
     for (int u = 0; u < kBulkBatch; ++u) {
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(512, 2) qcache_write_bulk_kernel(const QcacheW
       if (lane == 0) atomicMax(&blk_exp[((lo + i) >> p.sl) - blk0], x);
     }
   }
-  __syncthreads();
+  if (__syncthreads_or(failed)) return;  // (reported; nothing is written)
   if ((int)threadIdx.x < n_blk) {
     float* at = p.scales + (long long)b * p.n_blocks + blk0 + threadIdx.x;
     float scale = exp_to_float(blk_exp[threadIdx.x]), by = 1.f;

@@ -712,7 +712,7 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
     a.status[threadIdx.x] = 0;
     __threadfence();
   }
-  __syncwarp();
+  __syncthreads();
   grid_dep_launch();
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* as = smem;

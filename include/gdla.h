@@ -339,11 +339,11 @@ gdla_status gdla_gates(const gdla_gates_args* args, void* stream);
  * one head, shared by every query head, and e4m3 keeps its relative precision over
  * 14 powers of two, so one scale serves both parts of a row.
  *
- * Scales must be positive and finite. gdla_qcache_write sets each to the smallest
- * power of two (at least 2^-40) by which the block's largest magnitude is at most
- * 448, so that rows read back as bf16 are exact and a row's rounding does not depend
- * on its block. Rows that a call does not read or write may hold anything, NaN bit
- * patterns included, and so may their scales.
+ * Scales must be positive and finite (the decode takes one below 2^-60 as 2^-60).
+ * gdla_qcache_write sets each to the smallest power of two (at least 2^-40) by which
+ * the block's largest magnitude is at most 448, so that rows read back as bf16 are
+ * exact and a row's rounding does not depend on its block. Rows that a call does not
+ * read or write may hold anything, NaN bit patterns included, and so may their scales.
  *
  * Supported: d_c in {64, 128, 256, 512}, d_rope in {16, 32, 64} for write and read;
  * the head shapes of the other entry points for expand and decode; T_max up to
