@@ -458,11 +458,11 @@ def _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dt
     _same(lens, "lens", (B,), torch.int32)
     dev = c_cache.get_device()
     if c_hat_out is None:
-        c_hat_out = torch.empty((B, length, d_c), dtype=dtype, device=c_cache.device)
+        c_hat_out = c_cache.new_empty((B, length, d_c), dtype=dtype)
     else:
         _same(c_hat_out, "c_hat_out", (B, length, d_c), dtype)
     if k_rope_out is None:
-        k_rope_out = torch.empty((B, length, d_rope), dtype=dtype, device=c_cache.device)
+        k_rope_out = c_cache.new_empty((B, length, d_rope), dtype=dtype)
     else:
         _same(k_rope_out, "k_rope_out", (B, length, d_rope), dtype)
     a = _abi.QcacheReadArgs(B, length, T_max, first, d_c, d_rope, scale_block, n_kv, d_nope, d_v, _DT[dtype],
@@ -491,7 +491,7 @@ def qcache_expand(c_cache, kr_cache, scales, w_ukv, *, n_kv: int, d_nope: int, d
     shape = (c_cache.shape[0], length, n_kv, d_nope + d_v)
     _same(w_ukv, "w_ukv", (c_cache.shape[-1], n_kv * (d_nope + d_v)))
     if kv_out is None:
-        kv_out = torch.empty(shape, dtype=dtype, device=c_cache.device)
+        kv_out = w_ukv.new_empty(shape)
     else:
         _same(kv_out, "kv_out", shape, dtype)
     a, dev, c, k = _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out,
@@ -527,7 +527,7 @@ def qcache_decode(c_cache, kr_cache, scales, q, w_ukv, rope_cos, rope_sin, lam_l
     _same(rope_cos, "rope_cos", (rope_cos.shape[0], d_rope // 2), torch.float32)
     _same(rope_sin, "rope_sin", (rope_cos.shape[0], d_rope // 2), torch.float32)
     if out is None:
-        out = torch.empty((B, g * n_kv, d_v), dtype=q.dtype, device=q.device)
+        out = q.new_empty((B, g * n_kv, d_v))
     else:
         _same(out, "out", (B, g * n_kv, d_v), q.dtype)
     dev = c_cache.get_device()
