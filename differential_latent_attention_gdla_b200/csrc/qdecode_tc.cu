@@ -12,11 +12,21 @@
 // 8-bit MMA of this width is that of its shared-memory reads), and the two halves are added
 // when the accumulator is read:
 //   * q~ / 2^k, 2^k chosen for each head: its largest element fills the e4m3 range;
-//   * w = 2^(S + log2 s_j - M + 6) <= 2^8.75 < 448. The smallest step kept is 2^-13, 2^-19 of
-//     the largest weight (2^-22 when M lags): next to the rounding of the other weights, which
-//     is relative, this matters only for weights that add up to nothing.
+//   * w = 2^(S + log2 s_j - M + 6) <= 2^8.75 < 448. Its rounding is relative down to 2^-6;
+//     below, the step is 2^-13, and a weight under 2^-14 is lost. That counts where many small
+//     weights stand behind few large ones (a sink over a long flat context), so:
+//     - Where M has risen by 2^6 at least to a tile's maximum, and then at most 16 of the tile's
+//       weights are 2^-6 and more, all the others smaller by 2^8 at least and an eighth of those
+//       within 2^8 of their largest (a crowd; in a broad softmax they add up to nothing), M goes
+//       to 2^4 times that largest. The few go around the MMA: they are added to O^T in fp32.
+//     - At every 8th tile M goes down to 2^4 times the tile's largest weight where all of them
+//       are below 2^-6 and a crowd. Until then a tile's 128 weights lose 2^-13 of the largest
+//       weight at most.
+//     M stays within 2^60 of the largest reference before: O^T and the sum hold 2^66 and more.
+//     Logits of 1 / 2 / 4 / 8 nats deviation, 64 x 32768 tokens, 48 heads: 289 / 350 / 455 / 590
+//     us a call (280 / 330 / 349 / 346 with an M that only rises, and its lost weights).
 // A scale enters twice, both times outside the products: it multiplies the score, and it
-// is part of the weight (the reference M is the running maximum of S + log2 s). The sum of
+// is part of the weight (the reference M follows the maxima of S + log2 s). The sum of
 // 2^S is kept in fp32 from the weights before their rounding.
 //
 // Split: the visible 128-token tiles of all sequences are numbered in sequence order, and
@@ -57,6 +67,14 @@ constexpr int PBYTES = TT * 128;               // weights: TT tokens x (hi, lo) 
 constexpr uint32_t COL_S = 0;                  // S^T; then O^T of M-tile mt at NQ (1 + mt)
 constexpr float kBase = 6.f;                   // weights are 2^(S + log2 s - M + kBase)
 constexpr float kThr = 2.75f;                  // M moves when exceeded by this: w <= 2^8.75 < 448
+constexpr float kLow = -6.f;                   // weights from 2^kLow on are rounded relatively
+constexpr int kFew = 16;                       // tokens of a tile that may go around the MMA
+constexpr float kGap = 8.f;                    // and how far the others are below them
+constexpr int kCrowd = 8;                      // a crowd: 1 / 8 within 2^kGap of the largest
+constexpr float kRise = 6.f;                   // M has risen by this at least
+constexpr float kRoom = 4.f;                   // M over the others then: the next tiles' maxima vary
+constexpr int kLook = 8;                       // tiles from one look down to the next
+constexpr float kSpan = 60.f;                  // M goes down this far at most
 constexpr float kMinScale = 8.6736174e-19f;    // 2^-60: keeps 1/s finite whatever the scales hold
 
 // the layout for head groups of 16 HG heads
@@ -78,7 +96,19 @@ struct Lay {
     long long red[NT / 32];
     float4 hx[NH / 4], hm[NH / 4];  // per head: scale of the query; kBase - M
     float wmax[4][NH];
-    float alpha[NH];
+    float alpha[NH], move[NH];  // of a moved reference: 2^(old - new); the old less the new
+    // a moving reference: of each warp the tokens at 2^kLow and above (as a mask), the smallest
+    // S + log2 s of these, how many are below; the largest reference of the sequence share
+    uint32_t big[4][NH];
+    float wmin[4][NH];
+    int small[4][NH];
+    float top[NH];
+    int n_out[NH];                  // tokens of the tile that go around the MMA
+    // the same for the groups: the warps' tokens that some head takes out; a batch of them and
+    // their weights
+    uint32_t out_mask[HG][4];
+    int out_row[HG][kFew];
+    float4 out_w[HG][kFew][HT / 4];
   };
   static constexpr int SMEM = OFF_SH + (int)sizeof(Shared);
   static_assert(QIMG % 1024 == 0 && TILE % 1024 == 0, "1024-byte swizzle atoms");
@@ -193,8 +223,9 @@ __device__ __forceinline__ void score_mmas(uint32_t smem, uint32_t tmem) {
 #pragma unroll
   for (int kk = 0; kk < 2; ++kk) mma_f8_ss(tmem + COL_S, c64 + 2 * kk, q64 + 2 * kk, id, 1);
 }
+// (O^T starts from the zeros that the softmax warps write)
 template <int HG, int ST>
-__device__ __forceinline__ void value_mmas(uint32_t smem, uint32_t tmem, uint32_t acc) {
+__device__ __forceinline__ void value_mmas(uint32_t smem, uint32_t tmem) {
   using namespace sm100;
   using L = Lay<HG>;
   constexpr uint32_t id = idesc_f8_f32(128, L::NQ, kF8E4m3, kF8E4m3, true, true);
@@ -204,7 +235,7 @@ __device__ __forceinline__ void value_mmas(uint32_t smem, uint32_t tmem, uint32_
   for (int kk = 0; kk < TT / 32; ++kk)  // 32 tokens: 4096 bytes of a box and of the weights
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt)
-      mma_f8_ss(tmem + L::NQ * (1 + mt), c + ((mt * BOX + kk * 4096) >> 4), wd + ((kk * 4096) >> 4), id, kk ? 1u : acc);
+      mma_f8_ss(tmem + L::NQ * (1 + mt), c + ((mt * BOX + kk * 4096) >> 4), wd + ((kk * 4096) >> 4), id, 1u);
 }
 
 }  // namespace q8
@@ -383,16 +414,15 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
           idle = 0;
         }
         // the weights of tile kv are written; their softmax has also read the previous sequence's
-        // O^T, so a new sequence may overwrite it
+        // O^T and cleared it
         if (kv < ks && mbar_try_wait(smem_u32(&sh.p_full), kv & 1)) {
           const long long t = start + kv;
           wv.seek(t);
-          const uint32_t acc = kv > 0 && t != wv.pb;
           tc_fence_after();
           if (kv & 1)
-            value_mmas<HG, 1>(smem_u32(smem), tmem, acc);
+            value_mmas<HG, 1>(smem_u32(smem), tmem);
           else
-            value_mmas<HG, 0>(smem_u32(smem), tmem, acc);
+            value_mmas<HG, 0>(smem_u32(smem), tmem);
           mma_commit(smem_u32(&sh.empty[kv % STAGES]));
           mma_commit(smem_u32(&sh.p_free));
           if (kv == n_tiles - 1 || t == wv.pb + wv.st.n - 1) mma_commit(smem_u32(&sh.seg_done));  // O^T holds the share
@@ -446,6 +476,15 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
     float* hm1 = reinterpret_cast<float*>(hm);
     auto grp_or = [&](bool pred) { return named_bar_or(1 + grp, 128, pred); };
     auto grp_sync = [&]() { named_bar_sync(1 + grp, 128); };
+    auto clear_o = [&]() {  // O^T of the sequence that comes
+      uint32_t zero[HT];
+#pragma unroll
+      for (int h = 0; h < HT; ++h) zero[h] = 0;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) tmem_st16(tmem + lane_base + NQ * (1 + (c >> 1)) + NH * (c & 1) + hb, zero);
+      tmem_wait_st();
+    };
+    clear_o();
     Walker w, wn;
     w.init(a, b0, p0);
     wn.init(a, b0, p0);
@@ -474,7 +513,8 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
           const float* hs = reinterpret_cast<const float*>(
               a.qimg + ((long long)w.b * a.n_hg + hg) * a.img_bytes + L::QIMG);
           reinterpret_cast<float*>(hx)[tl] = hs[hb + tl];
-          hm1[tl] = INFINITY;
+          hm1[tl] = kBase;
+          sh.top[hb + tl] = -INFINITY;  // (no reference yet)
         }
 #pragma unroll
         for (int i = 0; i < HT / 2; ++i) lp[i] = make_float2(0.f, 0.f);
@@ -492,7 +532,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
       }
       bad |= !mbar_wait(smem_u32(&sh.s_full), k & 1, a.status, 522, &abort_flag);
       __syncwarp();
-      float2 dot[HT / 2], e[HT / 2];
+      float2 e[HT / 2];
       {
         tc_fence_after();
         uint32_t xh[HT], xl[HT];
@@ -502,10 +542,9 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
         tc_fence_before();
         mbar_arrive_warp(smem_u32(&sh.s_free));
 #pragma unroll
-        for (int i = 0; i < HT / 2; ++i) dot[i] = ffma2(f2(xl, i), make_float2(0.0625f, 0.0625f), f2(xh, i));
+        for (int i = 0; i < HT / 2; ++i)
+          e[i] = ffma2(ffma2(f2(xl, i), make_float2(0.0625f, 0.0625f), f2(xh, i)), fa[i], fb[i]);
       }
-#pragma unroll
-      for (int i = 0; i < HT / 2; ++i) e[i] = ffma2(dot[i], fa[i], fb[i]);
       if (!valid) {  // (whatever the row held)
 #pragma unroll
         for (int i = 0; i < HT / 2; ++i) e[i] = make_float2(-INFINITY, -INFINITY);
@@ -513,46 +552,147 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
       float mx = fmaxf(e[0].x, e[0].y);
 #pragma unroll
       for (int i = 1; i < HT / 2; ++i) mx = fmax3(mx, e[i].x, e[i].y);
-      if (grp_or(mx > kBase + kThr || bad)) {
+      bool look = false;
+      if (k % kLook == kLook - 1) {
+        float mn = INFINITY;
+#pragma unroll
+        for (int i = 0; i < HT / 2; ++i) mn = fmin3(mn, e[i].x, e[i].y);
+        if (__any_sync(0xffffffffu, valid && mn < kLow)) {
+#pragma unroll
+          for (int i = 0; i < HT; ++i)  // a head without any above, in this warp at least
+            look |= !__any_sync(0xffffffffu, (i & 1 ? e[i / 2].y : e[i / 2].x) >= kLow);
+          look = look && __any_sync(0xffffffffu, valid);
+        }
+      }
+      if (grp_or(mx > kBase + kThr || first || look || bad)) {
         if (grp_or(bad)) {
           ok = false;
           break;
         }
-        // some head's reference has to move: each that can goes to the tile's maximum of S + log2 s
+        // Some head's reference may have to move. It goes up to the tile's maximum of S + log2 s
+        auto e1 = [&](int i) { return i & 1 ? e[i / 2].y : e[i / 2].x; };
+        auto v1 = [&](int i) { return e1(i) - hm1[i]; };  // S + log2 s
+        const int h1 = hb + (tl & (HT - 1));  // threads below HT: their head
+        auto tile_max = [&]() { return fmaxf(fmaxf(sh.wmax[0][h1], sh.wmax[1][h1]), fmaxf(sh.wmax[2][h1], sh.wmax[3][h1])); };
 #pragma unroll
-        for (int i = 0; i < HT / 2; ++i) {
-          float2 v = ffma2(dot[i], fmul2(pair(hx, i), s2), ls2);
-          if (!valid) v = make_float2(-INFINITY, -INFINITY);
-          v.x = warp_max(v.x);
-          v.y = warp_max(v.y);
-          if (lane == 0) {
-            sh.wmax[q4][hb + 2 * i] = v.x;
-            sh.wmax[q4][hb + 2 * i + 1] = v.y;
+        for (int i = 0; i < HT; ++i) {
+          const float v = warp_max(v1(i));  // (-inf where the token is not visible)
+          if (lane == 0) sh.wmax[q4][hb + i] = v;
+        }
+        look = grp_or(look);
+        if (look) {
+#pragma unroll
+          for (int i = 0; i < HT; ++i) {
+            const int h = hb + i;
+            const float tm = fmaxf(fmaxf(sh.wmax[0][h], sh.wmax[1][h]), fmaxf(sh.wmax[2][h], sh.wmax[3][h]));
+            const uint32_t near = __ballot_sync(0xffffffffu, valid && v1(i) >= tm - kGap);
+            if (lane == 0) sh.small[q4][h] = __popc(near);
           }
+          grp_sync();
         }
-        grp_sync();
+        float m_old = 0.f, ref = 0.f;
         bool resc = false;
+        auto move_to = [&](float to) {
+          sh.move[h1] = ref - to;
+          ref = to;
+          resc = !first && ref != m_old;
+          sh.alpha[h1] = first ? 0.f : ex2_approx(m_old - ref);
+          hm1[tl] = kBase - ref;
+        };
         if (tl < HT) {
-          const int h = hb + tl;
-          const float tm = fmaxf(fmaxf(sh.wmax[0][h], sh.wmax[1][h]), fmaxf(sh.wmax[2][h], sh.wmax[3][h]));
-          const float m_old = kBase - hm1[tl];
-          const bool up = tm > m_old;  // (also when m_old is -inf and tm is not)
-          resc = up && m_old > -INFINITY;
-          sh.alpha[h] = ex2_approx(up ? m_old - tm : 0.f);  // (0 from -inf)
-          if (up) hm1[tl] = kBase - tm;
+          const float tm = tile_max();
+          m_old = ref = kBase - hm1[tl];
+          float to = ref;
+          if (tm > m_old || (first && tm > -INFINITY)) {  // (a first tile of NaN leaves it at 0)
+            to = tm;
+          } else if (look && tm < m_old + (kLow - kBase)) {
+            const int near = (sh.small[0][h1] + sh.small[1][h1]) + (sh.small[2][h1] + sh.small[3][h1]);
+            const int seen = min(w.st.Tb, w.token0(t) + TT) - max(w.st.lo, w.token0(t));
+            if (near * kCrowd >= seen) to = tm + kRoom;
+          }
+          move_to(fmaxf(to, sh.top[h1] - kSpan));
+          sh.top[h1] = fmaxf(sh.top[h1], ref);
         }
-        const bool any = grp_or(resc);  // (also publishes hm and alpha)
+        bool any = grp_or(resc);  // (also publishes hm and alpha)
+        auto rescore = [&]() {
 #pragma unroll
-        for (int i = 0; i < HT / 2; ++i) {
-          lp[i] = fmul2(lp[i], make_float2(sh.alpha[hb + 2 * i], sh.alpha[hb + 2 * i + 1]));
-          e[i] = ffma2(dot[i], fmul2(pair(hx, i), s2), fadd2(pair(hm, i), ls2));
-          if (!valid) e[i] = make_float2(-INFINITY, -INFINITY);
+          for (int i = 0; i < HT / 2; ++i) e[i] = fadd2(e[i], make_float2(sh.move[hb + 2 * i], sh.move[hb + 2 * i + 1]));
+        };
+        rescore();
+        float low = INFINITY;
+#pragma unroll
+        for (int i = 0; i < HT / 2; ++i) low = fmin3(low, e[i].x, e[i].y);
+        bool few = false, out = false;
+        if (__any_sync(0xffffffffu, valid && low < kLow)) {
+          // kFew of a full tile: some warp has kFew / 4 at most
+          const int lim = w.token0(t) >= w.st.lo && w.token0(t) + TT <= w.st.Tb ? kFew / 4 : kFew;
+#pragma unroll
+          for (int i = 0; i < HT; ++i)
+            few |= __popc(__ballot_sync(0xffffffffu, e1(i) >= kLow)) <= lim && valid && e1(i) < kLow &&
+                   (first || sh.move[hb + i] <= -kRise);
         }
-        if (any) {
-          // O^T holds the tiles before k once the value MMAs of tile k - 1 have landed
+        if (grp_or(few)) {
+          // the few that are far above all the others
+#pragma unroll
+          for (int i = 0; i < HT; ++i) {
+            const float v = v1(i), x = e1(i);
+            const uint32_t big = __ballot_sync(0xffffffffu, x >= kLow);
+            const uint32_t small = __ballot_sync(0xffffffffu, valid && x < kLow);
+            const float mx_small = warp_max(x < kLow ? v : -INFINITY);
+            const float mn_big = -warp_max(x >= kLow ? -v : -INFINITY);
+            if (lane == 0) {
+              sh.big[q4][hb + i] = big;
+              sh.small[q4][hb + i] = __popc(small);
+              sh.wmax[q4][hb + i] = mx_small;
+              sh.wmin[q4][hb + i] = mn_big;
+            }
+          }
+          grp_sync();
+          int n_big = 0, n_small = 0;
+          float rest = 0.f, lower = 0.f;
+          if (tl < HT) {
+            for (int q = 0; q < 4; ++q) {
+              n_big += __popc(sh.big[q][h1]);
+              n_small += sh.small[q][h1];
+            }
+            const float over = fminf(fminf(sh.wmin[0][h1], sh.wmin[1][h1]), fminf(sh.wmin[2][h1], sh.wmin[3][h1]));
+            rest = tile_max();
+            lower = fmaxf(rest + kRoom, sh.top[h1] - kSpan);
+            out = n_big > 0 && n_big <= min(kFew, n_small) && over - rest >= kGap && lower < ref;
+            sh.wmin[0][h1] = out ? rest - kGap : INFINITY;
+            sh.n_out[h1] = 0;
+            sh.move[h1] = 0.f;
+          }
+          if (grp_or(out)) {
+#pragma unroll
+            for (int i = 0; i < HT; ++i) {
+              const uint32_t near = __ballot_sync(0xffffffffu, e1(i) < kLow && v1(i) >= sh.wmin[0][hb + i]);
+              if (lane == 0) sh.small[q4][hb + i] = __popc(near);
+            }
+            grp_sync();
+            if (tl < HT) {
+              const int near = (sh.small[0][h1] + sh.small[1][h1]) + (sh.small[2][h1] + sh.small[3][h1]);
+              out = out && near * kCrowd >= n_small;
+              if (out) {
+                sh.n_out[h1] = n_big;
+                move_to(lower);
+              }
+            }
+          }
+          out = grp_or(out);
+          any = grp_or(resc);
+          rescore();
+        }
+#pragma unroll
+        for (int i = 0; i < HT / 2; ++i)
+          lp[i] = fmul2(lp[i], make_float2(sh.alpha[hb + 2 * i], sh.alpha[hb + 2 * i + 1]));
+        // O^T holds the tiles before k once the value MMAs of tile k - 1 have landed
+        if ((any || out) && k >= 1) {
           bad |= !mbar_wait(smem_u32(&sh.p_free), (k - 1) & 1, a.status, 523, &abort_flag);
           __syncwarp();
           tc_fence_after();
+        }
+        if (any) {
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {  // M-tile c / 2, hi or lo columns
             uint32_t o[HT];
@@ -564,6 +704,68 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
             tmem_st16(ta, o);
           }
           tmem_wait_st();
+        }
+        if (out) {
+          // this token's weights where it is one of the few; those go into the sum here, and to
+          // O^T in the order of the tokens, a batch of kFew tokens at a time
+          uint32_t mine = 0;
+#pragma unroll
+          for (int i = 0; i < HT; ++i)
+            if (sh.n_out[hb + i] > 0) mine |= ((sh.big[q4][hb + i] >> lane) & 1u) << i;
+          const uint32_t mask = __ballot_sync(0xffffffffu, mine != 0);
+          if (lane == 0) sh.out_mask[grp][q4] = mask;
+          // (the tile's rows, which only the MMAs have waited for so far)
+          bad |= !mbar_wait(smem_u32(&sh.full[k % STAGES]), (k / STAGES) & 1, a.status, 526, &abort_flag);
+          __syncwarp();
+          grp_sync();
+          int at = __popc(mask & ((1u << lane) - 1u)), n = 0;
+          for (int q = 0; q < 4; ++q) {
+            if (q < q4) at += __popc(sh.out_mask[grp][q]);
+            n += __popc(sh.out_mask[grp][q]);
+          }
+#pragma unroll 1
+          for (int n0 = 0; n0 < n; n0 += kFew) {
+            if (mine && at >= n0 && at < n0 + kFew) {
+              float* to = reinterpret_cast<float*>(sh.out_w[grp][at - n0]);
+              sh.out_row[grp][at - n0] = tl;
+#pragma unroll
+              for (int i = 0; i < HT; ++i) {
+                const bool one = (mine >> i) & 1u;
+                float& x = i & 1 ? e[i / 2].y : e[i / 2].x;
+                float& l = i & 1 ? lp[i / 2].y : lp[i / 2].x;
+                const float p = one ? ex2_approx(x) : 0.f;
+                to[i] = p;
+                l = fmaf(p, inv_s, l);
+                if (one) x = -INFINITY;  // (its weight in the MMA is 0)
+              }
+            }
+            grp_sync();
+#pragma unroll 1
+            for (int mt = 0; mt < 4; ++mt) {
+              uint32_t o[HT];
+              const uint32_t ta = tmem + lane_base + NQ * (1 + mt) + hb;
+              tmem_ld16(ta, o);
+              tmem_wait_ld();
+              const uint8_t* box = tiles + (k % STAGES) * TILE + mt * BOX;
+#pragma unroll 1
+              for (int u = 0; u < min(kFew, n - n0); ++u) {
+                const int r = sh.out_row[grp][u];  // row r, column tl of the box
+                const uint32_t byte = box[r * 128 + (((tl >> 4) ^ (r & 7)) << 4) + (tl & 15)];
+                const float c = __low2float(e4m3x2_to_half2(byte));
+#pragma unroll
+                for (int q = 0; q < HT / 4; ++q) {
+                  const float4 p = sh.out_w[grp][u][q];
+                  o[4 * q] = __float_as_uint(fmaf(p.x, c, __uint_as_float(o[4 * q])));
+                  o[4 * q + 1] = __float_as_uint(fmaf(p.y, c, __uint_as_float(o[4 * q + 1])));
+                  o[4 * q + 2] = __float_as_uint(fmaf(p.z, c, __uint_as_float(o[4 * q + 2])));
+                  o[4 * q + 3] = __float_as_uint(fmaf(p.w, c, __uint_as_float(o[4 * q + 3])));
+                }
+              }
+              tmem_st16(ta, o);
+            }
+            tmem_wait_st();
+            grp_sync();
+          }
         }
       }
       // weights of this token: hi and lo bytes of 16 heads
@@ -638,6 +840,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
           for (int h = 0; h < HT; ++h)
             if (hb + h < nh) dst[h * DC] = fmaf(__uint_as_float(ol[h]), 0.0625f, __uint_as_float(oh[h]));
         }
+        clear_o();
         tc_fence_before();
         grp_sync();
       }
@@ -994,7 +1197,7 @@ __global__ void __launch_bounds__(q8::CB_T, 1)
     float den = 0.f;
 #pragma unroll
     for (int q = 0; q < kPL; ++q) {
-      // (a share whose every score was NaN has M = -inf and l = NaN, and passes it on)
+      // (an l that is NaN, of a share that saw one, is passed on)
       const float f = v[q].x == -INFINITY ? 1.f : exp2f(v[q].x - M);
       den += f * v[q].y;
       v[q].x = f;

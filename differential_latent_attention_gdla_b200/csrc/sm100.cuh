@@ -325,6 +325,11 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // two fp32 lanes per instruction: (a.x*b.x + c.x, a.y*b.y + c.y) and (a.x + b.x, a.y + b.y),
 // each rounded like the scalar fmaf / add
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {

@@ -685,3 +685,95 @@ def test_refusals_on_the_device():
         gdla.qcache_read(c8, kr8, sc, length=64, first=1)
     with pytest.raises(ValueError):
         gdla.qcache_read(c8, kr8, sc[:1], length=64)
+
+
+# ------------------------------------------------------- a sink over a flat tail
+def sink_inputs(T, n_kv, g, nb, gap, sinks, size, B=1, seed=70):
+    """Sequences whose sink tokens score ``gap`` powers of two above all the others, which are
+    nearly flat and share a common component; the sinks' own latents are ``size`` of theirs.
+    The gap comes from two rotary columns whose products are exact in every operand type
+    (tau log2e is 2^-4, the tables rotate by nothing), so that no rounding of a score moves it."""
+    s = decode_inputs(B, T, n_kv, g, 512, 64, 128, "bf16", nb, [T] * B, seed, q_size=0.25)
+    gen = gen_for(seed + 1)
+    c = 1.0 + torch.randn((B, T, 512), generator=gen)
+    k = torch.zeros((B, T, 64))
+    whole = int(gap) // 2 * 2
+    for b in range(B):
+        c[b, sinks] *= size
+        k[b, sinks, 0], k[b, sinks, 1] = float(whole), (gap - whole) * 16
+    gdla.qcache_write(*s["cache"], c.to(DEV), k.to(DEV), scale_block=nb)
+    s["q"][..., 128:] = 0
+    s["q"][..., 128], s["q"][..., 129] = 16.0, 1.0
+    s["cos"], s["sin"] = torch.ones_like(s["cos"]), torch.zeros_like(s["sin"])
+    s["tau"] = float(np.log(2.0)) / 16
+    return s
+
+
+def sink_ref(s, window=0, kv_sel=None):
+    v = held(*s["cache"], s["nb"])
+    return np.stack([oracle.decode_seq(c_hat=v[b, :n, :512].copy(), k_r_rot=v[b, :n, 512:].copy(), q=f64(s["q"][b]),
+                                       w_ukv=f64(s["w"]), lam=f64(s["lam"][b]), gate=f64(s["gate"][b]), g=s["g"],
+                                       d_n=128, d_v=128, mask=mask_code("sliding" if window else "causal"),
+                                       window=window, scale=s["tau"], inv_freq=np.zeros(32), kv_sel=kv_sel)
+                     for b, n in enumerate(s["lens"])])
+
+
+# a share of one tile, of some, and of 14336 tokens (24 head groups: 6 shares of the cache)
+SINKS = [
+    dict(T=128, n_kv=2, g=2, nb=64, sinks=[0]),
+    dict(T=97, n_kv=2, g=2, nb=16, sinks=[96]),
+    dict(T=1500, n_kv=16, g=2, nb=1, sinks=[3]),
+    dict(T=1500, n_kv=16, g=2, nb=64, sinks=[0, 1, 2, 700, 1400]),
+    dict(T=2000, n_kv=16, g=4, nb=128, sinks=list(range(300, 316))),
+    dict(T=40000, n_kv=2, g=2, nb=64, sinks=[39999]),
+    dict(T=86016, n_kv=128, g=8, nb=64, sinks=[0]),
+]
+
+
+@pytest.mark.parametrize("case", SINKS, ids=lambda c: f"T{c['T']}_kv{c['n_kv']}_g{c['g']}_nb{c['nb']}_n{len(c['sinks'])}")
+@pytest.mark.parametrize("gap", [12.0, 18.0, 19.5, 20.0, 21.0, 30.0])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -8, 1.0])
+def test_decode_sink_over_a_flat_tail(case, gap, size):
+    # each other token weighs next to nothing, all of them together do not: the parity bar as it
+    # is, for the 8-bit and the bf16 cache of the same values
+    s = sink_inputs(**case, gap=gap, size=size)
+    sel = [0, case["n_kv"] - 1] if case["n_kv"] > 16 else None
+    ref = sink_ref(s, kv_sel=sel)
+    y = call_decode(s, softmax_scale=s["tau"])
+    assert_parity(f64(y), ref, torch.bfloat16, f"8-bit decode, sink {gap} {size} T={case['T']}")
+    c, k = gdla.qcache_read(*s["cache"], length=case["T"], scale_block=case["nb"])
+    y16 = gdla.decode(c, k, s["q"], s["w"], s["cos"], s["sin"], s["lam"], s["gate"], i32(s["lens"]), g=case["g"],
+                      softmax_scale=s["tau"])
+    assert_parity(f64(y16), ref, torch.bfloat16, f"bf16 decode, sink {gap} {size} T={case['T']}")
+
+
+@pytest.mark.parametrize("gap", [16.0, 18.0, 20.0])
+def test_decode_long_tail_behind_many_large_weights(gap):
+    # 40 tokens of the first tile, of small values, carry most of the softmax: the reference is
+    # theirs until it follows the tail, 8 of the 112 tiles of the first share at most
+    s = sink_inputs(86016, 128, 8, 64, gap, list(range(40)), 2.0 ** -6, seed=72)
+    ref = sink_ref(s, kv_sel=[0, 127])
+    assert_parity(f64(call_decode(s, softmax_scale=s["tau"])), ref, torch.bfloat16, f"8-bit decode, 40 sinks {gap}")
+
+
+@pytest.mark.parametrize("q_size", [0.5, 2.0, 4.0, 8.0])
+@pytest.mark.parametrize("T,lens", [(9000, [9000, 8000]), (700, [700, 129])])
+def test_decode_broad_softmax(T, lens, q_size):
+    # logits of half a nat to eight of deviation: the reference rises often, and the tiles are
+    # looked at; a logit of size s moves by s 2^-8 (the query's two 8-bit terms)
+    s = decode_inputs(2, T, 3, 2, 512, 64, 128, "bf16", 16, lens, seed=73, q_size=q_size)
+    ref = decode_ref(s)
+    assert_parity(f64(call_decode(s)), ref, torch.bfloat16, f"8-bit decode, logits x {q_size}",
+                  elem_bound=0.1 + 8 * (5 * q_size) * 2.0 ** -8)
+
+
+@pytest.mark.parametrize("window", [0, 700])
+def test_decode_sinks_in_a_batch(window):
+    # sinks inside and in front of the window, at tile borders; several sequences in one share
+    s = sink_inputs(900, 2, 1, 64, 20.0, [0, 127, 128, 500, 899], 0.0, B=60, seed=71)
+    s["lens"] = [900 - 13 * (i % 7) for i in range(60)]
+    ref = sink_ref(s, window)
+    poison(s, window)
+    y = call_decode(s, window, softmax_scale=s["tau"])
+    assert_parity(f64(y), ref, torch.bfloat16, f"8-bit decode, sinks in a batch, window {window}")
+    assert torch.equal(call_decode(s, window, softmax_scale=s["tau"]), y)
