@@ -178,7 +178,7 @@ bool decode_uses_tc(const gdla_decode_args* a) {
 }
 
 struct DecodeLayout {
-  size_t status, q_abs, q_rot, qimg, seqinfo, part_o, part_ml, total;
+  size_t status, failed, q_abs, q_rot, qimg, seqinfo, part_o, part_ml, total;
   int tc, n_splits, split_len, n_ranges, n_hg, hpc, part_heads, img_heads;
 };
 
@@ -807,6 +807,8 @@ static DecodeLayout qdecode_layout(const gdla_qcache_decode_args* a) {
   l.n_ranges = (int)std::min((long)std::max(1, kQdecSMs / l.n_hg), tiles_max);
   const size_t records = ((size_t)l.n_ranges + a->B) * l.n_hg;
   size_t off = kStatusBytes;
+  l.failed = off;
+  off = align256(off + sizeof(int) * (size_t)a->n_kv * qdec_absorb_tiles(a->B, a->g) * kQdecAbsorbSplit);
   l.qimg = off;
   off = align256(off + (size_t)a->B * l.n_hg * qdec_image_bytes(l.part_heads));
   l.seqinfo = off;
@@ -867,6 +869,7 @@ gdla_status gdla_qcache_decode(const gdla_qcache_decode_args* a, void* stream) {
   if (lay.tc) {
     d.qimg = (uint8_t*)(ws + lay.qimg);
     d.seqinfo = (int2*)(ws + lay.seqinfo);
+    p.failed = (int*)(ws + lay.failed);
   } else {
     d.q_abs = (float*)(ws + lay.q_abs);
     d.q_rot = (float*)(ws + lay.q_rot);

@@ -147,12 +147,17 @@ cudaError_t launch_qcache_read(const QcacheReadParams& p, gdla_dtype dt, cudaStr
 constexpr int kQdecHeads = 48;
 constexpr int kQdecTile = 128;
 constexpr int kQdecSMs = 148;     // B200
+// the absorb kernel's grid: KV groups x tiles of query rows x CTAs of a cluster, each of which
+// leaves a word for the split kernel: 0, or how it failed
+constexpr int kQdecAbsorbRows = 128, kQdecAbsorbSplit = 4;
+__host__ __device__ constexpr int qdec_absorb_tiles(int B, int g) { return (B * (g + 1) + kQdecAbsorbRows - 1) / kQdecAbsorbRows; }
 __host__ __device__ constexpr int qdec_image_data(int heads) { return 2 * heads * 576; }
 __host__ __device__ constexpr int qdec_image_bytes(int heads) { return (qdec_image_data(heads) + 4 * heads + 255) / 256 * 256; }
 struct QdecodeParams {
   DecodeParams d;
   const float* scales;
   int sl, n_blocks;
+  int* failed;
 };
 // Allows a kernel `bytes` of dynamic shared memory, once a device (`done`: one bit each)
 template <typename K>

@@ -35,7 +35,7 @@
 // combine kernel merges the records of a sequence.
 //
 // Block: warp 0 loads tiles (TMA, two stages of 72 KB), warp 1 issues the MMAs, warp 2 loads
-// query images, warp 3 idles; the others are the softmax, a group of four warps for each 16 of
+// query images, warp 3 reports what failed before; the others are the softmax, a group of four warps for each 16 of
 // the up to 48 heads: a thread owns one token (TMEM lane) and 16 heads, and the four warps of
 // a group agree on their heads' references by a barrier of their own. Every wait is bounded
 // and reports GDLA_ERR_TIMEOUT.
@@ -127,6 +127,8 @@ struct Args {
   float* part_o;   // [records][heads of a group][512]
   float* part_ml;  // [records][heads of a group][2]
   int* status;
+  const int* failed;  // of the absorb kernel's CTAs
+  int n_absorb;
 };
 
 // the visible tiles of a sequence: tokens [lo, Tb), tiles jt0 .. jt0 + n - 1
@@ -141,8 +143,17 @@ __device__ __forceinline__ SeqTiles seq_tiles(const Args& a, int b) {
   s.n = (int)(((long long)s.Tb + TT - 1) / TT) - s.jt0;
   return s;
 }
-// lengths outside [0, T_max] are clamped, and reported
-__device__ __forceinline__ void report_lengths(const Args& a, int t, int nt) {
+// failures of the absorb kernel's CTAs, as they are left in their records
+constexpr int kAbsorbLoad = 541, kAbsorbMma = 542, kAbsorbAlignment = 598;
+// these are reported, and lengths outside [0, T_max], which are clamped
+__device__ __forceinline__ void report(const Args& a, int t, int nt) {
+  for (int c = t; c < a.n_absorb; c += nt) {
+    const int code = a.failed[c];
+    if (code) {
+      atomicCAS(a.status, 0, (int)(code == kAbsorbAlignment ? GDLA_ERR_CUDA : GDLA_ERR_TIMEOUT));
+      atomicCAS(a.status + 1, 0, code);
+    }
+  }
   for (int b = t; b < a.B; b += nt) {
     const int raw = __ldg(a.seqlens + b);
     if (raw < 0 || raw > a.T_max) atomicCAS(a.status, 0, (int)GDLA_ERR_INVALID_ARG);
@@ -319,7 +330,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
   const int R = sh.R;
   if (start >= end || sh.b0 < 0) {  // a range beyond the tiles
     grid_dep_wait();                // (this grid never completes before the one it overlaps)
-    if (r == 0 && hg == 0) report_lengths(a, tid, NT);
+    if (r == 0 && hg == 0) report(a, tid, NT);
     return;
   }
   const int b0 = sh.b0;
@@ -446,8 +457,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
     }
   } else if (warp == 2) {
     // -------------------------------------------------------- query images
-    grid_dep_wait();  // the absorb kernel wrote them, and cleared the status word
-    if (r == 0 && hg == 0) report_lengths(a, lane, 32);
+    grid_dep_wait();  // the absorb kernel wrote them
     if (lane == 0) {
       Walker w;
       w.init(a, b0, p0);
@@ -465,7 +475,10 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
       if (!ok) abort_flag = 1;
       if (seg > 0) mbar_wait(smem_u32(&sh.q_full), (seg - 1) & 1, nullptr, 0);  // no copy is in flight at exit
     }
-  } else if (warp >= 4) {
+  } else if (warp == 3) {
+    grid_dep_wait();  // the absorb kernel cleared the status word
+    if (r == 0 && hg == 0) report(a, lane, 32);
+  } else {
     // ------------------------------------------------------------- softmax
     const int grp = (warp - 4) >> 2, q4 = warp & 3, hb = grp * HT;
     const int tl = q4 * 32 + lane;  // this thread's token of the tile; its index in the group
@@ -860,7 +873,8 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
 // of a row is exchanged through distributed shared memory, so that the row is scaled by one
 // power of two and written once. Each CTA adds a quarter of the rotary part.
 namespace q8 {
-constexpr int AB = 128;
+constexpr int AB = kQdecAbsorbRows;
+static_assert(DC / AB == kQdecAbsorbSplit, "one CTA of the cluster for each 128 columns");
 constexpr int AB_OP = AB * AB * 2;  // an operand: two 64-column chunks of [128 rows x 128 B]
 constexpr int AB_SMEM = 2 * AB_OP + 64;
 struct AbsorbArgs {
@@ -872,6 +886,7 @@ struct AbsorbArgs {
   const float* sin_tab;
   uint8_t* qimg;
   int* status;
+  int* failed;
 };
 // byte of dimension d of image row (hi: head; lo: NH + head)
 __device__ __forceinline__ int image_offset(int NH, int row, int d) {
@@ -910,7 +925,10 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
     qdecode_absorb_kernel(const __grid_constant__ CUtensorMap tmW, const q8::AbsorbArgs a) {
   using namespace sm100;
   using namespace q8;
-  // the call's status word, before any kernel of the call can report to it
+  // The call's status word, before the split kernel can report to it. Nothing orders this store
+  // and the other CTAs of this grid, so they neither read the word nor report to it: each leaves
+  // its own record of a failure (0: none), which the split kernel reports
+  int* const failed = a.failed + (blockIdx.y * gridDim.x + blockIdx.x) * gridDim.z + blockIdx.z;
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x < kStatusBytes / 4) {
     a.status[threadIdx.x] = 0;
     __threadfence();
@@ -922,6 +940,7 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
   uint8_t* bs = smem + AB_OP;
   uint64_t* bar = reinterpret_cast<uint64_t*>(smem + 2 * AB_OP);  // [0] W landed, [1] MMAs done
   __shared__ uint32_t tmem_slot;
+  __shared__ int w_landed;
   __shared__ float part_max[2][AB], row_max[AB];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int h = blockIdx.x, z = blockIdx.z;
@@ -929,13 +948,11 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
   const int NH = a.NH, img_data = qdec_image_data(NH), img_bytes = qdec_image_bytes(NH);
   // (the cluster's CTAs have the same shared-memory layout: all four or none pass this)
   if (smem_u32(smem) & 1023u) {
-    if (tid == 0) {
-      atomicCAS(a.status, 0, (int)GDLA_ERR_CUDA);
-      atomicCAS(a.status + 1, 0, 598);
-    }
+    if (tid == 0) *failed = kAbsorbAlignment;
     return;
   }
   if (tid == 0) {
+    w_landed = 0;
     mbar_init(smem_u32(&bar[0]), 1);
     mbar_init(smem_u32(&bar[1]), 1);
     fence_mbar_init();
@@ -969,7 +986,8 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   if (tid == 32) {
-    if (mbar_wait(smem_u32(&bar[0]), 0, a.status, 541)) {
+    if (mbar_wait(smem_u32(&bar[0]), 0, nullptr, 0)) {
+      w_landed = 1;
       tc_fence_after();
       constexpr uint32_t id = idesc_bf16_f32(AB, AB, false, false);
 #pragma unroll
@@ -1011,7 +1029,7 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
 #pragma unroll
     for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fmaxf(fabsf(lo[e]), fabsf(hi[e])));
   }
-  const bool done = mbar_wait(smem_u32(&bar[1]), 0, a.status, 542);
+  const bool done = mbar_wait(smem_u32(&bar[1]), 0, nullptr, 0);
   __syncwarp();
   tc_fence_after();
   uint32_t v0[32], v1[32];
@@ -1038,7 +1056,7 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
     ex = max((int)(u >> 23) - 127 - ((u & 0x7FFFFFu) <= 0x600000u ? 8 : 7), -100);
   }
   const float inv = __int_as_float((127 - ex) << 23);
-  if (real && done && !earlier_failure(a.status)) {
+  if (real && done && w_landed) {
     const int hgi = head / a.hpc, lh = head - hgi * a.hpc;
     uint8_t* img = a.qimg + ((long long)b * a.n_hg + hgi) * img_bytes;
     // (an infinity would saturate: a query that is not finite gives NaN, as its scores would)
@@ -1079,8 +1097,9 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
   }
   cluster_sync();  // (no CTA of the cluster leaves while another reads its row maxima)
   tc_fence_before();
-  __syncthreads();
+  const bool all_done = __syncthreads_and(done);
   tc_fence_after();
+  if (tid == 0) *failed = !w_landed ? kAbsorbLoad : !all_done ? kAbsorbMma : 0;
   if (warp == 0) tmem_dealloc(tmem, AB);
 }
 
@@ -1353,12 +1372,12 @@ cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s) {
     a.NH = d.part_heads;
     a.isc = d.scale * kLog2e;
     a.q = reinterpret_cast<const __nv_bfloat16*>(d.q); a.seqlens = d.seqlens; a.cos_tab = d.cos_tab;
-    a.sin_tab = d.sin_tab; a.qimg = d.qimg; a.status = d.status;
+    a.sin_tab = d.sin_tab; a.qimg = d.qimg; a.status = d.status; a.failed = p.failed;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(qdecode_absorb_kernel, AB_SMEM, allowed);
     if (e != cudaSuccess) return e;
-    const int rows = d.B * (d.g + 1);
-    qdecode_absorb_kernel<<<dim3((unsigned)d.n_kv, (unsigned)((rows + AB - 1) / AB), DC / AB), 256, AB_SMEM, s>>>(tw, a);
+    const unsigned tiles = (unsigned)qdec_absorb_tiles(d.B, d.g);
+    qdecode_absorb_kernel<<<dim3((unsigned)d.n_kv, tiles, kQdecAbsorbSplit), 256, AB_SMEM, s>>>(tw, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -1378,6 +1397,7 @@ cudaError_t launch_qdecode_tc(const QdecodeParams& p, cudaStream_t s) {
     a.img_bytes = qdec_image_bytes(d.part_heads); a.seqlens = d.seqlens;
     a.c8 = (const uint8_t*)d.c_cache; a.kr8 = (const uint8_t*)d.kr_cache; a.scales = p.scales; a.qimg = d.qimg;
     a.seqinfo = d.seqinfo; a.part_o = d.part_o; a.part_ml = d.part_ml; a.status = d.status;
+    a.failed = p.failed; a.n_absorb = d.n_kv * qdec_absorb_tiles(d.B, d.g) * kQdecAbsorbSplit;
     const dim3 grid((unsigned)d.n_hg, (unsigned)d.n_ranges);
     cudaError_t e;
     switch (d.part_heads / HT) {

@@ -777,3 +777,23 @@ def test_decode_sinks_in_a_batch(window):
     y = call_decode(s, window, softmax_scale=s["tau"])
     assert_parity(f64(y), ref, torch.bfloat16, f"8-bit decode, sinks in a batch, window {window}")
     assert torch.equal(call_decode(s, window, softmax_scale=s["tau"]), y)
+
+
+# ------------------------------------------------------- what a workspace held before
+STALE = [_abi.GDLA_ERR_TIMEOUT, _abi.GDLA_ERR_CUDA, _abi.GDLA_ERR_INVALID_ARG, -1]
+
+
+@pytest.mark.parametrize("code", STALE)
+def test_decode_in_a_workspace_of_a_failed_call(code):
+    # the status word of the call before, and every other word, say nothing to this one: the query
+    # images are written whatever they hold
+    for B, n_kv, g in ((3, 16, 2), (200, 16, 4)):
+        s = decode_inputs(B, 140, n_kv, g, 512, 64, 128, "bf16", 1, [1 + (37 * b) % 140 for b in range(B)], seed=80)
+        want = call_decode(s)
+        need = gdla.qcache_decode_workspace_size(B=B, T_max=140, d_c=512, d_rope=64, n_kv=n_kv, d_nope=128, d_v=128, g=g)
+        ws = torch.empty(need // 4, dtype=torch.int32, device=DEV)
+        for _ in range(10):
+            ws.fill_(code)
+            y = call_decode(s, workspace=ws)
+            assert gdla.workspace_status(ws) == _abi.GDLA_OK
+            assert torch.equal(y, want)
