@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(512, sizeof(T) == 2 && (!KEEP || TPW == 1) ? 2
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
   const int b = blockIdx.y;
   const int SB = 1 << p.sl, WU = min(SB, n_warps), UPC = n_warps / WU;
-  // the first CTA sets the status word, in the place of a memset in front of the kernel
+  // the first CTA sets the status word, in the place of a memset in front of the kernel (no other
+  // reads it or reports to it)
   if (blockIdx.x == 0 && b == 0) {
     bool bad = false;
     for (int i = threadIdx.x; i < p.B; i += blockDim.x) bad |= !range_ok(p, i);
@@ -411,11 +412,12 @@ __global__ void __launch_bounds__(512, 2) qcache_write_bulk_kernel(const QcacheW
   __shared__ float first_by;  // factor of the first block's earlier rows, 1 if they stay
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int b = blockIdx.y, C = 1 << lc;
+  // (the status word is cleared before the kernel: its CTAs' waits read it)
   if (blockIdx.x == 0 && b == 0) {
     bool bad = false;
     for (int i = threadIdx.x; i < p.B; i += blockDim.x) bad |= !range_ok(p, i);
     bad = __syncthreads_or(bad);
-    if (threadIdx.x < kStatusBytes / 4) p.status[threadIdx.x] = threadIdx.x == 0 && bad ? (int)GDLA_ERR_INVALID_ARG : 0;
+    if (threadIdx.x == 0 && bad) atomicCAS(p.status, 0, (int)GDLA_ERR_INVALID_ARG);
   }
   if (!range_ok(p, b)) return;
   const int n = p.lens ? p.lens[b] : p.L, p0 = p.start ? p.start[b] : 0;
@@ -600,6 +602,7 @@ cudaError_t write_bulk(const QcacheWriteParams& p, int lc, size_t smem, cudaStre
   auto k = qcache_write_bulk_kernel<__nv_bfloat16>;
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(k, kBulkMaxSmem, allowed);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p.status, 0, kStatusBytes, s);
   if (e != cudaSuccess) return e;
   const long long chunks = (((long long)p.L + (1 << lc) - 2) >> lc) + 1;
   k<<<dim3((unsigned)chunks, (unsigned)p.B), smem > (size_t)(60 << 10) ? 512 : 256, smem, s>>>(p, lc);

@@ -797,3 +797,26 @@ def test_decode_in_a_workspace_of_a_failed_call(code):
             y = call_decode(s, workspace=ws)
             assert gdla.workspace_status(ws) == _abi.GDLA_OK
             assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("code", STALE)
+@pytest.mark.parametrize("L", [1, 300, 6000])
+def test_write_in_a_workspace_of_a_failed_call(code, L):
+    gen = gen_for(81)
+    c = torch.randn((3, L, 512), generator=gen).bfloat16().to(DEV)
+    k = torch.randn((3, L, 64), generator=gen).bfloat16().to(DEV)
+    want = gdla.qcache_empty(3, L, scale_block=16, device=DEV)
+    gdla.qcache_write(*want, c, k, scale_block=16)
+    ws = torch.empty(64, dtype=torch.int32, device=DEV)
+    for _ in range(10):
+        got = gdla.qcache_empty(3, L, scale_block=16, device=DEV)
+        for t in got:
+            t.view(torch.uint8).fill_(0x55)
+        ws.fill_(code)
+        gdla.qcache_write(*got, c, k, scale_block=16, workspace=ws)
+        assert gdla.workspace_status(ws) == _abi.GDLA_OK
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+    # a range that does not fit is reported whatever the word held
+    ws.fill_(code)
+    gdla.qcache_write(*got, c, k, scale_block=16, lens=i32([L, L, L]), start=i32([0, 1, 0]), workspace=ws)
+    assert gdla.workspace_status(ws) == _abi.GDLA_ERR_INVALID_ARG
