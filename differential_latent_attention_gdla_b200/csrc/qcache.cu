@@ -488,8 +488,12 @@ __global__ void __launch_bounds__(512, 2) qcache_write_bulk_kernel(const QcacheW
         }
       }
     }
-    if (!landed) failed = !(landed = sm100::mbar_wait(sm100::smem_u32(&bar), 0, p.status, 561));
-    __syncwarp();
+    // the first of a warp's rounds waits for the chunk; a warp that gives up looks at none of it
+    if (!landed) landed = sm100::mbar_wait(sm100::smem_u32(&bar), 0, p.status, 561);
+    if (!__all_sync(0xffffffffu, landed)) {
+      failed = true;
+      break;
+    }
 #pragma unroll
     for (int u = 0; u < kBulkBatch; ++u) {
       float2 x[8], s2 = make_float2(0.f, 0.f);
