@@ -545,7 +545,10 @@ __global__ void __launch_bounds__(512, 2) qcache_write_bulk_kernel(const QcacheW
       if (lane == 0) atomicMax(&blk_exp[((lo + i) >> p.sl) - blk0], x);
     }
   }
-  if (__syncthreads_or(failed)) return;  // (reported; nothing is written)
+  if (__syncthreads_or(failed)) {  // (reported; nothing is written)
+    if (threadIdx.x == 0) sm100::mbar_wait(sm100::smem_u32(&bar), 0, nullptr, 0);  // no copy is in flight at exit
+    return;
+  }
   if ((int)threadIdx.x < n_blk) {
     float* at = p.scales + (long long)b * p.n_blocks + blk0 + threadIdx.x;
     float scale = exp_to_float(blk_exp[threadIdx.x]), by = 1.f;

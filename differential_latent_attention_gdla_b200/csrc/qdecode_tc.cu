@@ -389,9 +389,9 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
         for (int bx = 0; bx < 4; ++bx) tma_load_3d(dst + bx * BOX, &tmC, bar, bx * 128, j0, wl.b);
         tma_load_3d(dst + 4 * BOX, &tmR, bar, 0, j0, wl.b);
       }
-      if (abort_flag)
-        for (int q = (k > STAGES ? k - STAGES : 0); q < k; ++q)
-          mbar_wait(smem_u32(&sh.full[q % STAGES]), (q / STAGES) & 1, nullptr, 0);
+      // no copy is in flight at exit, also where another warp gives up after the last load
+      for (int q = (k > STAGES ? k - STAGES : 0); q < k; ++q)
+        mbar_wait(smem_u32(&sh.full[q % STAGES]), (q / STAGES) & 1, nullptr, 0);
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMAs
@@ -996,6 +996,8 @@ __global__ void __cluster_dims__(1, 1, 4) __launch_bounds__(256, 1)
         mma_ss(tmem, sdesc_sw128(smem_u32(as + (kk >> 2) * (AB_OP / 2)) + off, 16, 1024),
                sdesc_sw128(smem_u32(bs + (kk >> 2) * (AB_OP / 2)) + off, 16, 1024), id, kk > 0);
       }
+    } else {
+      mbar_wait(smem_u32(&bar[0]), 0, nullptr, 0);  // no copy is in flight at exit
     }
     mma_commit(smem_u32(&bar[1]));
   }
@@ -1285,6 +1287,8 @@ __global__ void __launch_bounds__(q8::CB_T, 1)
       for (int kk = 0; kk < DC / 16; ++kk)
         mma_ss(tmem, sdesc_sw128(smem_u32(as + (kk >> 2) * (64 * 128)) + (kk & 3) * 32, 16, 1024),
                sdesc_sw128(smem_u32(bs) + kk * 2048, CB_B / 2, 1024), id, kk > 0);
+    } else {
+      mbar_wait(smem_u32(&bar[0]), 0, nullptr, 0);  // no copy is in flight at exit
     }
     mma_commit(smem_u32(&bar[1]));
   }
