@@ -6,9 +6,9 @@
 //   s   = the smallest power of two >= 2^-40 with max |c|, |k| of the block <= 448 s,
 //   row = e4m3([c | k] / s), round to nearest even, once.
 // A scale moves by a factor of two where the block's maximum passes 448 2^e. The maximum is
-// formed in fp32, to 2^-19; a token whose maximum comes nearer than 2^-18 to such a border
-// (one in some 90,000) is looked at again in 64 bits, so that the choice does not depend on
-// the order of a sum. Elements are rounded from values that are off by a few 2^-24.
+// formed in fp32, to 2^-19; a token whose maximum comes nearer than 2^-16 to such a border
+// (one in some 20,000 of normally distributed ones), or is past fp32's range, is looked at
+// again in 64 bits, so that the choice does not depend on the order of a sum. Elements are rounded from values that are off by a few 2^-24.
 //
 // Bound by the bytes: 1152 in and 576 out per bf16 token of the report's sizes.
 #include <cuda_fp8.h>
@@ -81,11 +81,12 @@ __device__ __forceinline__ F warp_sum(F x) {
   for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
-// the same of an fp32 value that is off by 2^-19 at most, and whether the border is too near
-// to tell (128 steps of 2^-23)
+// the same of an fp32 value that is off by 2^-19 at most, and whether fp32 cannot tell: the
+// border is too near (128 steps of 2^-23), or the value is past fp32's range
 __device__ __forceinline__ int scale_exp_fast(float top, bool& near) {
   const uint32_t u = __float_as_uint(top);
-  if (u >= 0x7F800000u) return kQcacheMinExp;  // (a NaN asks for nothing; an infinity is `odd`)
+  near |= u == 0x7F800000u;
+  if (u >= 0x7F800000u) return kQcacheMinExp;  // (a NaN asks for nothing)
   const int k = (int)(u >> 23) - 127, m = (int)(u & 0x7FFFFFu) - 0x600000;
   near |= m > -128 && m < 128;
   return max(m <= 0 ? k - 8 : k - 7, kQcacheMinExp);

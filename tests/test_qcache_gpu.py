@@ -820,3 +820,28 @@ def test_write_in_a_workspace_of_a_failed_call(code, L):
     ws.fill_(code)
     gdla.qcache_write(*got, c, k, scale_block=16, lens=i32([L, L, L]), start=i32([0, 1, 0]), workspace=ws)
     assert gdla.workspace_status(ws) == _abi.GDLA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("dt,L", [("bf16", 5), ("fp32", 5), ("bf16", 17000)])
+def test_write_maxima_past_fp32(dt, L):
+    # a normalised latent past fp32's range (one element of many, a large gain): its block takes
+    # the scale that it needs, and what is stored is its value over that
+    gen = gen_for(82)
+    c = 0.01 * torch.randn((1, L, 64), generator=gen)
+    c[0, 1::2] = 0
+    c[0, 1::2, 7] = 0.16
+    c = c.to(DT[dt])
+    gamma = torch.ones(64).to(DT[dt])
+    gamma[7] = 3e38
+    cos, sin = gdla.rope_tables(L, 16, device=DEV)
+    cache = gdla.qcache_empty(1, L, d_c=64, d_rope=16, device=DEV)
+    gdla.qcache_write(*cache, c.to(DEV), torch.zeros((1, L, 16), dtype=DT[dt], device=DEV), gamma=gamma.to(DEV),
+                      rope_cos=cos, rope_sin=sin)
+    x = f64(c)[0]
+    x = x / np.sqrt((x * x).mean(-1, keepdims=True) + 1e-6) * f64(gamma)
+    top = np.abs(x).max(-1)
+    assert top[1] > 2.0 ** 128 and top[0] > 0
+    e = np.frexp(top / 448)
+    want = np.maximum(np.where(e[0] == 0.5, np.exp2(e[1] - 1.0), np.exp2(e[1] * 1.0)), 2.0 ** -40)
+    assert (f64(cache[2])[0] == want).all()
+    assert_quantised(e4m3_values(cache[0])[0], x, want[:, None])
