@@ -840,6 +840,8 @@ static gdla_status validate_qdecode(const gdla_qcache_decode_args* a) {
 
 size_t gdla_qcache_decode_workspace_size(const gdla_qcache_decode_args* a) {
   if (!a || a->B < 1 || a->T_max < 1 || a->n_kv < 1 || a->g < 1) return 0;
+  // (what no call takes, and the layout's 32-bit products of heads do not hold)
+  if (a->B > 65535 || a->T_max > kQcacheMaxTokens || a->n_kv > 65535 || a->g > 8) return 0;
   return qdecode_layout(a).total;
 }
 

@@ -450,6 +450,7 @@ typedef struct {
   size_t workspace_bytes;
 } gdla_qcache_decode_args;
 
+/* (0 for sizes that no call takes) */
 size_t gdla_qcache_decode_workspace_size(const gdla_qcache_decode_args* args);
 gdla_status gdla_qcache_decode(const gdla_qcache_decode_args* args, void* stream);
 
