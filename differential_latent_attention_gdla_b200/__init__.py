@@ -514,7 +514,7 @@ def qcache_decode(c_cache, kr_cache, scales, q, w_ukv, rope_cos, rope_sin, lam_l
     A sequence of length 0 (an empty slot of a padded batch) returns zeros."""
     B, T_max, d_c, d_rope = _qcache_dims(c_cache, kr_cache, scales, scale_block)
     H_q, d_qk = q.shape[1], q.shape[2]
-    if H_q % (g + 1):
+    if g < 1 or H_q < 1 or H_q % (g + 1):
         raise ValueError("q must hold g*n_noise signal heads followed by n_noise noise heads")
     n_kv = H_q // (g + 1)
     d_nope = d_qk - d_rope

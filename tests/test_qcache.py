@@ -192,3 +192,13 @@ def test_binding_rejects_before_the_library():
             gdla.qcache_decode(c8, kr8, sc, q, **{**args, **bad}, g=2, scale_block=16)
     with pytest.raises(ValueError, match="noise heads"):
         gdla.qcache_decode(c8, kr8, sc, q, **args, g=4, scale_block=16)
+
+
+@pytest.mark.parametrize("g,heads", [(0, 6), (-1, 6), (-2, 6), (6, 6), (2, 0)])
+def test_binding_rejects_head_counts(g, heads):
+    # (g = -1: no division by g + 1 = 0)
+    c8, kr8, sc = gdla.qcache_empty(2, 100, d_c=64, d_rope=16, scale_block=16, device="cpu")
+    tab = torch.zeros((100, 8))
+    with pytest.raises(ValueError, match="noise heads"):
+        gdla.qcache_decode(c8, kr8, sc, torch.zeros((2, heads, 48)), torch.zeros((64, 128)), tab, tab, torch.zeros((2, 4)),
+                           torch.zeros((2, 4, 32)), torch.ones(2, dtype=torch.int32), g=g, scale_block=16)
