@@ -344,7 +344,8 @@ def decode_noalloc(c_cache, kr_cache, q, w_ukv, rope_cos, rope_sin, lam_logits, 
 # ----------------------------------------------------------- 8-bit latent cache
 # (These calls are a decode step's, several a layer, so the binding's own time counts: the
 # stream comes as a raw handle where torch offers one, 0.1 us against 2 to 3, and a tensor's
-# device, layout and address are read together.)
+# device, layout and address are read together. What a call allocates by itself belongs to the
+# stream that it is given: an output that is used on another one is the caller's to record there.)
 _Q8 = (torch.float8_e4m3fn, torch.uint8)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
@@ -399,6 +400,18 @@ def _ptrs(device: int, *tensors):
     return out
 
 
+def _new(like, shape, dtype, stream):
+    """Memory on the device of ``like`` for a call on ``stream``: of that stream where one is given,
+    so that neither what the current stream still does to freed memory nor what it allocates
+    next meets the call."""
+    if stream is None or not like.is_cuda:  # (the device's current stream, which is the call's)
+        return like.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def _call(fn, a, device: int, stream, what):
     """The call with CUDA device ``device`` current, on ``stream`` or that device's current stream."""
     if stream is not None:
@@ -442,7 +455,7 @@ def qcache_write(c_cache, kr_cache, scales, c_kv, k_rope, *, gamma=None, rope_co
         _same(rope_cos, "rope_cos", (max_pos, d_rope // 2), torch.float32)
         _same(rope_sin, "rope_sin", (max_pos, d_rope // 2), torch.float32)
     if workspace is None:
-        workspace = torch.empty(256, dtype=torch.uint8, device=c_kv.device)
+        workspace = _new(c_kv, 256, torch.uint8, stream)
     dev = c_cache.get_device()
     a = _abi.QcacheWriteArgs(B, L, T_max, d_c, d_rope, scale_block, _dtype(c_kv), rms_eps, max_pos,
                              *_ptrs(dev, c_kv, gamma, k_rope, rope_cos, rope_sin, start, lens, c_cache, kr_cache, scales,
@@ -450,19 +463,19 @@ def qcache_write(c_cache, kr_cache, scales, c_kv, k_rope, *, gamma=None, rope_co
     _call(_lib().gdla_qcache_write, a, dev, stream, "gdla_qcache_write")
 
 
-def _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out, n_kv=0,
-                 d_nope=0, d_v=0, w_ukv=None, kv_out=None):
+def _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out, stream,
+                 n_kv=0, d_nope=0, d_v=0, w_ukv=None, kv_out=None):
     B, T_max, d_c, d_rope = _qcache_dims(c_cache, kr_cache, scales, scale_block)
     if dtype not in _DT:
         raise ValueError(f"unsupported dtype {dtype}; GDLA takes bfloat16 or float32")
     _same(lens, "lens", (B,), torch.int32)
     dev = c_cache.get_device()
     if c_hat_out is None:
-        c_hat_out = c_cache.new_empty((B, length, d_c), dtype=dtype)
+        c_hat_out = _new(c_cache, (B, length, d_c), dtype, stream)
     else:
         _same(c_hat_out, "c_hat_out", (B, length, d_c), dtype)
     if k_rope_out is None:
-        k_rope_out = c_cache.new_empty((B, length, d_rope), dtype=dtype)
+        k_rope_out = _new(c_cache, (B, length, d_rope), dtype, stream)
     else:
         _same(k_rope_out, "k_rope_out", (B, length, d_rope), dtype)
     a = _abi.QcacheReadArgs(B, length, T_max, first, d_c, d_rope, scale_block, n_kv, d_nope, d_v, _DT[dtype],
@@ -476,7 +489,8 @@ def qcache_read(c_cache, kr_cache, scales, *, length: int, first: int = 0, lens=
     ``dtype`` values: (c_hat [B,length,d_c], k_rope [B,length,d_rope]). With
     ``lens`` (int32 [B] on the device) only the first lens[b] of them are read;
     the others are zeros."""
-    a, dev, c, k = _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out)
+    a, dev, c, k = _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out,
+                                stream)
     _call(_lib().gdla_qcache_read, a, dev, stream, "gdla_qcache_read")
     return c, k
 
@@ -491,11 +505,11 @@ def qcache_expand(c_cache, kr_cache, scales, w_ukv, *, n_kv: int, d_nope: int, d
     shape = (c_cache.shape[0], length, n_kv, d_nope + d_v)
     _same(w_ukv, "w_ukv", (c_cache.shape[-1], n_kv * (d_nope + d_v)))
     if kv_out is None:
-        kv_out = w_ukv.new_empty(shape)
+        kv_out = _new(w_ukv, shape, dtype, stream)
     else:
         _same(kv_out, "kv_out", shape, dtype)
     a, dev, c, k = _qcache_read(c_cache, kr_cache, scales, length, first, lens, scale_block, dtype, c_hat_out, k_rope_out,
-                                n_kv, d_nope, d_v, w_ukv, kv_out)
+                                stream, n_kv, d_nope, d_v, w_ukv, kv_out)
     _call(_lib().gdla_qcache_expand, a, dev, stream, "gdla_qcache_expand")
     return kv_out, k, c
 
@@ -527,14 +541,13 @@ def qcache_decode(c_cache, kr_cache, scales, q, w_ukv, rope_cos, rope_sin, lam_l
     _same(rope_cos, "rope_cos", (rope_cos.shape[0], d_rope // 2), torch.float32)
     _same(rope_sin, "rope_sin", (rope_cos.shape[0], d_rope // 2), torch.float32)
     if out is None:
-        out = q.new_empty((B, g * n_kv, d_v))
+        out = _new(q, (B, g * n_kv, d_v), q.dtype, stream)
     else:
         _same(out, "out", (B, g * n_kv, d_v), q.dtype)
     dev = c_cache.get_device()
     if workspace is None:
-        workspace = torch.empty(qcache_decode_workspace_size(B=B, T_max=T_max, d_c=d_c, d_rope=d_rope, n_kv=n_kv,
-                                                             d_nope=d_nope, d_v=d_v, g=g, dtype=q.dtype),
-                                dtype=torch.uint8, device=q.device)
+        workspace = _new(q, qcache_decode_workspace_size(B=B, T_max=T_max, d_c=d_c, d_rope=d_rope, n_kv=n_kv, d_nope=d_nope,
+                                                         d_v=d_v, g=g, dtype=q.dtype), torch.uint8, stream)
     a = _abi.QcacheDecodeArgs(B, T_max, d_c, d_rope, n_kv, d_nope, d_v, n_kv, g, scale_block, _mask(mask), window,
                               softmax_scale, _dtype(q), rope_cos.shape[0],
                               *_ptrs(dev, seqlens, c_cache, kr_cache, scales, q, w_ukv, rope_cos, rope_sin, lam_logits,

@@ -845,3 +845,44 @@ def test_write_maxima_past_fp32(dt, L):
     want = np.maximum(np.where(e[0] == 0.5, np.exp2(e[1] - 1.0), np.exp2(e[1] * 1.0)), 2.0 ** -40)
     assert (f64(cache[2])[0] == want).all()
     assert_quantised(e4m3_values(cache[0])[0], x, want[:, None])
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_defaults_on_a_given_stream(handle):
+    # What a call allocates by itself is its stream's. The given stream is held up, so that the call's
+    # kernels run after the current stream has taken and filled memory of the same sizes; and the
+    # current stream is, so that it still writes to memory that was freed before the call.
+    B, T = 4, 600
+    s = decode_inputs(B, T, 16, 2, 512, 64, 128, "bf16", 16, [600, 1, 300, 77], seed=90)
+    c_kv = torch.randn((B, T, 512), generator=gen_for(91)).bfloat16().to(DEV)
+    k_rope = torch.randn((B, T, 64), generator=gen_for(92)).bfloat16().to(DEV)
+    need = gdla.qcache_decode_workspace_size(B=B, T_max=T, d_c=512, d_rope=64, n_kv=16, d_nope=128, d_v=128, g=2)
+    side = torch.cuda.Stream()
+    lens = i32(s["lens"])
+
+    def calls(stream):
+        cache = [t.clone() for t in s["cache"]]
+        torch.cuda.synchronize()
+        kw = {} if stream is None else {"stream": stream.cuda_stream if handle else stream}
+        for st in (stream, torch.cuda.current_stream()) if stream is not None else ():
+            with torch.cuda.stream(st):
+                torch.cuda._sleep(40_000_000)
+        sizes = (256, need, B * 32 * 128 * 2, B * T * 512 * 2, B * T * 64 * 2, B * T * 16 * 256 * 2)
+        freed = [torch.empty(n, dtype=torch.uint8, device=DEV) for n in sizes]
+        for t in freed:
+            t.fill_(0xFF)
+        del freed, t
+        gdla.qcache_write(*cache, c_kv, k_rope, scale_block=16, **kw)
+        out = [gdla.qcache_decode(*cache, s["q"], s["w"], s["cos"], s["sin"], s["lam"], s["gate"], lens, g=2,
+                                  scale_block=16, **kw)]
+        out += gdla.qcache_read(*cache, length=T, scale_block=16, **kw)
+        out += gdla.qcache_expand(*cache, s["w"], n_kv=16, d_nope=128, d_v=128, length=T, scale_block=16, **kw)
+        junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device=DEV) for n in sizes for _ in range(2)]
+        torch.cuda.synchronize()
+        del junk
+        return out
+
+    want = calls(None)
+    assert all(torch.isfinite(t.float()).all() for t in want)
+    for got, ref in zip(calls(side), want):
+        assert torch.equal(got, ref)
