@@ -886,3 +886,21 @@ def test_defaults_on_a_given_stream(handle):
     assert all(torch.isfinite(t.float()).all() for t in want)
     for got, ref in zip(calls(side), want):
         assert torch.equal(got, ref)
+
+
+# head groups of up to 16, 32 and 48 heads, full and padded, with sinks and without
+@pytest.mark.parametrize("n_kv,g", [(16, 1), (5, 4), (4, 3), (7, 1), (16, 3), (16, 4)])
+@pytest.mark.parametrize("gap", [0.0, 20.0])
+@pytest.mark.parametrize("nb", [1, 64])
+def test_decode_head_groups(n_kv, g, gap, nb):
+    s = sink_inputs(1100, n_kv, g, nb, gap, [0, 600, 601], 2.0 ** -4, B=2, seed=95)
+    s["lens"] = [1100, 650]
+    ref = sink_ref(s)
+    y = call_decode(s, softmax_scale=s["tau"])
+    assert_parity(f64(y), ref, torch.bfloat16, f"8-bit decode, {n_kv * (g + 1)} heads, sink {gap}")
+    # a share of several tiles gives what the same sequence alone gives, in one tile a share
+    many = {**s, "cache": [t[:1].expand(70, *t.shape[1:]).contiguous() for t in s["cache"]],
+            **{n: s[n][:1].expand(70, *s[n].shape[1:]).contiguous() for n in ("q", "lam", "gate")}, "lens": [1100] * 70}
+    ym = call_decode(many, softmax_scale=s["tau"])
+    for b in (0, 33, 69):
+        assert_parity(f64(ym[b]), ref[0], torch.bfloat16, f"8-bit decode, {n_kv * (g + 1)} heads, one of 70")
