@@ -10,7 +10,8 @@
 // (one in some 20,000 of normally distributed ones), or is past fp32's range, is looked at
 // again in 64 bits, so that the choice does not depend on the order of a sum. Elements are rounded from values that are off by a few 2^-24.
 //
-// Bound by the bytes: 1152 in and 576 out per bf16 token of the report's sizes.
+// The floor is the bytes: 1152 in and 576 out per bf16 token of the report's sizes, 37 us for
+// 131072 tokens; the kernel of many tokens takes 79, see there.
 #include <cuda_fp8.h>
 
 #include "common.cuh"

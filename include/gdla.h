@@ -425,6 +425,11 @@ gdla_status gdla_qcache_expand(const gdla_qcache_read_args* args, void* stream);
  * gdla_decode (bf16 with d_c = 512 and d_rope = 64 on the tensor cores in e4m3, with
  * any head count; other shapes and fp32 on the CUDA cores with at most 64 query
  * heads), and the same workspace rules.
+ * On the tensor cores the absorbed query and the softmax's weights are each the sum of
+ * two e4m3 values (relative rounding at most 2^-8; one bf16 value's is 2^-9). Weights
+ * too small for that next to the largest are kept where a crowd of them stands behind a
+ * few large ones or behind a stretch of the sequence (csrc/qdecode_tc.cu says how far),
+ * not in a broad softmax, where they add up to nothing.
  * A sequence of length 0 (an empty slot of a padded batch) returns zeros. A length
  * outside [0, T_max] is clamped into it and reported as GDLA_ERR_INVALID_ARG in the
  * status word. */
