@@ -15,16 +15,18 @@
 //   * w = 2^(S + log2 s_j - M + 6) <= 2^8.75 < 448. Its rounding is relative down to 2^-6;
 //     below, the step is 2^-13, and a weight under 2^-14 is lost. That counts where many small
 //     weights stand behind few large ones (a sink over a long flat context), so:
-//     - Where M has risen by 2^6 at least to a tile's maximum, and then at most 16 of the tile's
-//       weights are 2^-6 and more, all the others smaller by 2^8 at least and an eighth of those
-//       within 2^8 of their largest (a crowd; in a broad softmax they add up to nothing), M goes
-//       to 2^4 times that largest. The few go around the MMA: they are added to O^T in fp32.
+//     - Where M has risen by 2^6 at least to a tile's maximum, and then at most 64 of the tile's
+//       weights are 2^-6 and more and all the others smaller by 2^14 at least, or by 2^8 and a
+//       crowd (an eighth of them within 2^8 of their largest; in a broad softmax they add up to
+//       nothing), M goes to 2^4 times the largest of the others (2^8 if they are no crowd: then
+//       the tiles' maxima vary more). The few go around the MMA: they are added to O^T in fp32.
 //     - At every 8th tile M goes down to 2^4 times the tile's largest weight where all of them
 //       are below 2^-6 and a crowd. Until then a tile's 128 weights lose 2^-13 of the largest
 //       weight at most.
 //     M stays within 2^60 of the largest reference before: O^T and the sum hold 2^66 and more.
-//     Logits of 1 / 2 / 4 / 8 nats deviation, 64 x 32768 tokens, 48 heads: 289 / 350 / 455 / 590
-//     us a call (280 / 330 / 349 / 346 with an M that only rises, and its lost weights).
+//     Logits of 1 / 2 / 4 / 8 nats deviation, 64 x 32768 tokens, 48 heads: 296 / 355 / 422 / 651
+//     us a call (287 / 325 / 353 / 349 with an M that only rises, and its lost weights). What
+//     is not seen: several heights above the others with none of the gaps, whose values vanish.
 // A scale enters twice, both times outside the products: it multiplies the score, and it
 // is part of the weight (the reference M follows the maxima of S + log2 s). The sum of
 // 2^S is kept in fp32 from the weights before their rounding.
@@ -68,8 +70,10 @@ constexpr uint32_t COL_S = 0;                  // S^T; then O^T of M-tile mt at 
 constexpr float kBase = 6.f;                   // weights are 2^(S + log2 s - M + kBase)
 constexpr float kThr = 2.75f;                  // M moves when exceeded by this: w <= 2^8.75 < 448
 constexpr float kLow = -6.f;                   // weights from 2^kLow on are rounded relatively
-constexpr int kFew = 16;                       // tokens of a tile that may go around the MMA
+constexpr int kFew = 64;                       // tokens of a tile that may go around the MMA
+constexpr int kBatch = 16;                     // so many at a time
 constexpr float kGap = 8.f;                    // and how far the others are below them
+constexpr float kFar = 14.f;                   // so far below, they are kept even if they are no crowd
 constexpr int kCrowd = 8;                      // a crowd: 1 / 8 within 2^kGap of the largest
 constexpr float kRise = 6.f;                   // M has risen by this at least
 constexpr float kRoom = 4.f;                   // M over the others then: the next tiles' maxima vary
@@ -107,8 +111,8 @@ struct Lay {
     // the same for the groups: the warps' tokens that some head takes out; a batch of them and
     // their weights
     uint32_t out_mask[HG][4];
-    int out_row[HG][kFew];
-    float4 out_w[HG][kFew][HT / 4];
+    int out_row[HG][kBatch];
+    float4 out_w[HG][kBatch][HT / 4];
   };
   static constexpr int SMEM = OFF_SH + (int)sizeof(Shared);
   static_assert(QIMG % 1024 == 0 && TILE % 1024 == 0, "1024-byte swizzle atoms");
@@ -636,13 +640,18 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
 #pragma unroll
         for (int i = 0; i < HT / 2; ++i) low = fmin3(low, e[i].x, e[i].y);
         bool few = false, out = false;
-        if (__any_sync(0xffffffffu, valid && low < kLow)) {
-          // kFew of a full tile: some warp has kFew / 4 at most
+        float rise = INFINITY;
+#pragma unroll
+        for (int i = 0; i < HT; ++i) rise = fminf(rise, sh.move[hb + i]);
+        if ((first || rise <= -kRise) && __any_sync(0xffffffffu, valid && low < kLow)) {
+          // kFew of a full tile: some warp has kFew / 4 at most. (No branches between the votes)
           const int lim = w.token0(t) >= w.st.lo && w.token0(t) + TT <= w.st.Tb ? kFew / 4 : kFew;
 #pragma unroll
-          for (int i = 0; i < HT; ++i)
-            few |= __popc(__ballot_sync(0xffffffffu, e1(i) >= kLow)) <= lim && valid && e1(i) < kLow &&
-                   (first || sh.move[hb + i] <= -kRise);
+          for (int i = 0; i < HT; ++i) {
+            const int n_big = __popc(__ballot_sync(0xffffffffu, e1(i) >= kLow));
+            few |= (n_big <= lim) & (e1(i) < kLow) & (first | (sh.move[hb + i] <= -kRise));
+          }
+          few &= valid;
         }
         if (grp_or(few)) {
           // the few that are far above all the others
@@ -662,16 +671,18 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
           }
           grp_sync();
           int n_big = 0, n_small = 0;
-          float rest = 0.f, lower = 0.f;
+          float lower = 0.f;
+          bool far = false;
           if (tl < HT) {
             for (int q = 0; q < 4; ++q) {
               n_big += __popc(sh.big[q][h1]);
               n_small += sh.small[q][h1];
             }
             const float over = fminf(fminf(sh.wmin[0][h1], sh.wmin[1][h1]), fminf(sh.wmin[2][h1], sh.wmin[3][h1]));
-            rest = tile_max();
+            const float rest = tile_max();
+            far = over - rest >= kFar;
             lower = fmaxf(rest + kRoom, sh.top[h1] - kSpan);
-            out = n_big > 0 && n_big <= min(kFew, n_small) && over - rest >= kGap && lower < ref;
+            out = n_big > 0 && n_big <= kFew && n_small > 0 && over - rest >= kGap && lower < ref;
             sh.wmin[0][h1] = out ? rest - kGap : INFINITY;
             sh.n_out[h1] = 0;
             sh.move[h1] = 0.f;
@@ -685,10 +696,11 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
             grp_sync();
             if (tl < HT) {
               const int near = (sh.small[0][h1] + sh.small[1][h1]) + (sh.small[2][h1] + sh.small[3][h1]);
-              out = out && near * kCrowd >= n_small;
+              const bool crowd = near * kCrowd >= n_small;
+              out = out && (far || crowd);
               if (out) {
                 sh.n_out[h1] = n_big;
-                move_to(lower);
+                move_to(crowd ? lower : lower + kRoom);
               }
             }
           }
@@ -720,7 +732,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
         }
         if (out) {
           // this token's weights where it is one of the few; those go into the sum here, and to
-          // O^T in the order of the tokens, a batch of kFew tokens at a time
+          // O^T in the order of the tokens, a batch of tokens at a time
           uint32_t mine = 0;
 #pragma unroll
           for (int i = 0; i < HT; ++i)
@@ -737,8 +749,8 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
             n += __popc(sh.out_mask[grp][q]);
           }
 #pragma unroll 1
-          for (int n0 = 0; n0 < n; n0 += kFew) {
-            if (mine && at >= n0 && at < n0 + kFew) {
+          for (int n0 = 0; n0 < n; n0 += kBatch) {
+            if (mine && at >= n0 && at < n0 + kBatch) {
               float* to = reinterpret_cast<float*>(sh.out_w[grp][at - n0]);
               sh.out_row[grp][at - n0] = tl;
 #pragma unroll
@@ -761,7 +773,7 @@ __global__ void __launch_bounds__(q8::Lay<HG>::NT, 1)
               tmem_wait_ld();
               const uint8_t* box = tiles + (k % STAGES) * TILE + mt * BOX;
 #pragma unroll 1
-              for (int u = 0; u < min(kFew, n - n0); ++u) {
+              for (int u = 0; u < min(kBatch, n - n0); ++u) {
                 const int r = sh.out_row[grp][u];  // row r, column tl of the box
                 const uint32_t byte = box[r * 128 + (((tl >> 4) ^ (r & 7)) << 4) + (tl & 15)];
                 const float c = __low2float(e4m3x2_to_half2(byte));

@@ -904,3 +904,24 @@ def test_decode_head_groups(n_kv, g, gap, nb):
     ym = call_decode(many, softmax_scale=s["tau"])
     for b in (0, 33, 69):
         assert_parity(f64(ym[b]), ref[0], torch.bfloat16, f"8-bit decode, {n_kv * (g + 1)} heads, one of 70")
+
+
+@pytest.mark.parametrize("levels", [
+    [(40, [0], 0.0), (18, list(range(5, 17)), 0.125)],                                  # few behind a sink, and no crowd
+    [(24, list(range(60)), 0.0)],                                                       # half a tile of sinks
+    [(32, [0, 130, 131, 300], 0.0), (24, list(range(140, 180)), 2.0 ** -6)],
+    [(16, list(range(0, 400, 50)), 0.0), (30, [399], 0.0)],
+])
+@pytest.mark.parametrize("T", [320, 400])
+def test_decode_levels(levels, T):
+    # tokens at several heights above the others
+    s = sink_inputs(T, 5, 4, 128, 0.0, [], 1.0, seed=96)
+    gen = gen_for(97)
+    c, k = 1.0 + torch.randn((1, T, 512), generator=gen), torch.zeros((1, T, 64))
+    for gap, tokens, size in levels:
+        tokens = [t for t in tokens if t < T]
+        c[0, tokens] *= size
+        k[0, tokens, 0] = float(gap)
+    gdla.qcache_write(*s["cache"], c.to(DEV), k.to(DEV), scale_block=128)
+    y = call_decode(s, softmax_scale=s["tau"])
+    assert_parity(f64(y), sink_ref(s), torch.bfloat16, f"8-bit decode, levels {[g for g, *_ in levels]}")
