@@ -407,7 +407,9 @@ def _new(like, shape, dtype, stream):
     if stream is None or not like.is_cuda:  # (the device's current stream, which is the call's)
         return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream(stream), device=like.device)
+        handle = _stream(stream)  # (0 and 1: the default stream, which is no external one to torch)
+        stream = (torch.cuda.default_stream(like.device) if handle in (0, 1) else
+                  torch.cuda.ExternalStream(handle, device=like.device))
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 

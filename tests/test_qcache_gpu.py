@@ -925,3 +925,19 @@ def test_decode_levels(levels, T):
     gdla.qcache_write(*s["cache"], c.to(DEV), k.to(DEV), scale_block=128)
     y = call_decode(s, softmax_scale=s["tau"])
     assert_parity(f64(y), sink_ref(s), torch.bfloat16, f"8-bit decode, levels {[g for g, *_ in levels]}")
+
+
+def test_allocations_are_the_given_streams():
+    c8, kr8, sc = made_cache(2, 700, 512, 64, 16, seed=98)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream, want in ((side, side.cuda_stream), (side.cuda_stream, side.cuda_stream), (0, 0), (1, 0),
+                         (torch.cuda.default_stream(), 0)):
+        for current in (torch.cuda.default_stream(), torch.cuda.Stream()):
+            with torch.cuda.stream(current):
+                out = gdla.qcache_read(c8, kr8, sc, length=700, scale_block=16, stream=stream)
+            torch.cuda.synchronize()
+            for t in out:
+                at = [g for g in torch.cuda.memory_snapshot() if g["address"] <= t.data_ptr() < g["address"] + g["total_size"]]
+                assert [g["stream"] for g in at] == [want]
+            assert (np.concatenate([f64(t) for t in out], -1) == held(c8, kr8, sc, 16)).all()
