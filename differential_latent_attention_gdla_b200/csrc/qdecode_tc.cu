@@ -42,7 +42,7 @@
 // a group agree on their heads' references by a barrier of their own. Every wait is bounded
 // and reports GDLA_ERR_TIMEOUT.
 //
-// What bounds it (B=64 over 32768 tokens, 48 heads: this kernel 287 us, 4.2 TB/s of cache): a
+// What bounds it (B=64 over 32768 tokens, 48 heads: this kernel 286 us by itself, 4.2 TB/s of cache): a
 // tile's way through its stage -- load, scores (1015 cycles of shared-memory reads), softmax
 // (~1750), values (905) -- with two of them in flight; the loads alone run at the memory's
 // rate (without the MMAs: 211 us). Tried and slower: prefetches into L2 (337 us a call without,
